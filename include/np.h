@@ -361,6 +361,146 @@ np_status np_ffn_rows_noalloc(const float* h_dev, const void* w_gate, const void
  * holds an asynchronous CUDA error.  Allocates nothing. */
 np_status np_ffn_rows_noalloc_check(void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Key/value cache: the attention half of a decode step, next to the FFN calls
+ * above.  Keys and values are held in 8 bits (e4m3) in pages of NP_KV_PAGE
+ * tokens, with one scale per page and head, and a block table maps each
+ * sequence's tokens to pages.  Sequences may share pages (fork); a page is
+ * written only while one sequence holds it (np_kv_reserve copies it first).
+ *
+ * One step of a user's program: np_kv_reserve once (lengths grow by the new
+ * tokens, pages are assigned), then per layer np_kv_append (the new tokens'
+ * keys and values) and np_kv_attend (the new tokens' queries).  lengths count
+ * the new tokens from np_kv_reserve on: with n new tokens in a sequence of
+ * length L, append writes positions L-n .. L-1 and query i sits at L-n+i.
+ *
+ * All calls are asynchronous on `stream`, allocate nothing, read their index
+ * arguments on the device and can be captured into a graph.  Calls that
+ * change a cache (reserve, append, fork, release, compact) must not overlap
+ * on the GPU with other calls on the same cache; np_kv_attend calls may
+ * overlap each other as long as each has a workspace of its own.
+ *
+ * Errors that only the device can see (a row, length or page out of range, no
+ * free page left) are recorded in the cache's error word, work[0].  While it
+ * is set the calls that change the cache do nothing; np_kv_check reports and
+ * clears it.
+ * ------------------------------------------------------------------------- */
+#define NP_KV_PAGE 64       /* tokens per page and per scale */
+#define NP_KV_MAX_BATCH 1024 /* sequences in one call */
+
+/* A cache in caller-owned device memory (16-byte aligned; k, v 128-byte). */
+typedef struct {
+  int32_t n_layers;
+  int32_t n_pages;    /* pages in the pool */
+  int32_t n_kv_heads; /* key/value heads, 1..256 */
+  int32_t head_dim;   /* 64, 128 or 256 */
+  int32_t max_seqs;   /* rows of the block table */
+  int32_t max_pages;  /* its width: a sequence holds up to max_pages * NP_KV_PAGE tokens */
+  void* k;            /* e4m3 [n_layers][n_pages][n_kv_heads][NP_KV_PAGE][head_dim] */
+  void* v;            /* e4m3 [n_layers][n_pages][n_kv_heads][head_dim][NP_KV_PAGE] (transposed: the
+                         product with the softmax weights then reads contiguous tokens) */
+  float* k_scale;     /* [n_layers][n_pages][n_kv_heads]: value = code * scale */
+  float* v_scale;
+  int32_t* table;     /* [max_seqs][max_pages] page numbers, -1 where there is none */
+  int32_t* lengths;   /* [max_seqs] tokens held */
+  int32_t* refs;      /* [n_pages] sequences that hold the page; 0 = free */
+  int32_t* work;      /* np_kv_work_words() words of scratch; work[0] is the error word.  Zero
+                         before the first call */
+} np_kv_desc;
+
+/* The sequences of one np_kv_append / np_kv_attend call and their new tokens,
+ * packed one sequence after another in the call's token-major tensors. */
+typedef struct {
+  const int32_t* seqs; /* device [n_seqs]: table rows, each at most once; NULL: rows 0..n_seqs-1 */
+  const int32_t* cu;   /* device [n_seqs + 1]: sequence i's tokens are cu[i] .. cu[i+1]-1, cu[0] = 0;
+                          NULL: n_tokens / n_seqs tokens each.  Tokens from cu[n_seqs] on (the
+                          padding of a captured call) are neither read nor written */
+  int32_t n_seqs;      /* 1..NP_KV_MAX_BATCH */
+  int32_t n_tokens;    /* tokens in the tensors */
+  int32_t max_tokens;  /* no sequence has more new tokens than this (checked on the device) */
+} np_kv_batch;
+
+/* Words of scratch that np_kv_desc.work needs; -1 for a description that the
+ * calls would refuse (its pointers are not looked at). */
+int64_t np_kv_work_words(const np_kv_desc* kv);
+
+/* Room for n_new[i] more tokens (device int32 >= 0) in each listed sequence
+ * (seqs: device, each row at most once; NULL: rows 0..n-1): lengths grow by n_new and missing
+ * pages are taken from the free ones, lowest page number first, in list
+ * order.  If the first new token falls into a page that other sequences hold
+ * too, the sequence gets a copy of it (every layer); of several listed
+ * sequences that hold the same page the last one keeps it when no unlisted
+ * one holds it.  All or nothing: with too few free pages (NP_ERR_OOM), a
+ * table row too short or a bad row (NP_ERR_STATE) nothing changes and the
+ * error is recorded. */
+np_status np_kv_reserve(const np_kv_desc* kv, const int32_t* seqs, const int32_t* n_new, int32_t n, void* stream);
+
+/* Rows dst[i] become what rows src[i] were before the call (pages shared, not
+ * copied); what the dst rows held is given up.  dst rows are distinct, src
+ * rows need not be and may be dst rows (a reordering of search beams).
+ * A bad or repeated dst row: nothing changes, NP_ERR_STATE recorded. */
+np_status np_kv_fork(const np_kv_desc* kv, const int32_t* src, const int32_t* dst, int32_t n, void* stream);
+
+/* Give pages back.  window = 0: all pages of the listed sequences, whose
+ * lengths become 0.  window > 0: only those pages that no later query of the
+ * sequence sees under that window and `sinks` (their table entries become -1,
+ * lengths stay). A page is free when no sequence holds it any more. */
+np_status np_kv_release(const np_kv_desc* kv, const int32_t* seqs, int32_t n, int32_t window, int32_t sinks,
+                        void* stream);
+
+/* Pack the pool: with n pages in use, each free page below n (ascending) gets
+ * the contents of a used page from n on (ascending), one copy each, and the
+ * block table is renumbered; pages n.. are free afterwards. */
+np_status np_kv_compact(const np_kv_desc* kv, void* stream);
+
+/* Write the new tokens' keys and values of one layer.  k, v: [n_tokens]
+ * [n_kv_heads][head_dim] of `dtype` with the given strides in elements (the
+ * last dimension contiguous).  Per page and head the scale is the smallest
+ * power of two 2^e, -40 <= e <= 40, with amax <= 448 * 2^e over the tokens
+ * the page holds; codes are x / scale rounded to nearest, saturating.  When a
+ * later token raises a page's scale the codes there are rescaled (a power of
+ * two: only codes that become subnormal are rounded again).  A NaN in a key
+ * is kept; a token with a NaN in its value is stored with a NaN key and that
+ * element 0, so that every query that sees it gets NaN and no other does. */
+np_status np_kv_append(const np_kv_desc* kv, int32_t layer, const np_kv_batch* batch, const void* k,
+                       int64_t k_token_stride, int64_t k_head_stride, const void* v, int64_t v_token_stride,
+                       int64_t v_head_stride, int32_t dtype, void* stream);
+
+/* What np_kv_attend reads and writes. */
+typedef struct {
+  const void* q;             /* [n_tokens][n_heads][head_dim] of dtype */
+  void* out;                 /* the same; shares no memory with q */
+  int64_t q_token_stride;    /* strides in elements; the last dimension is contiguous */
+  int64_t q_head_stride;
+  int64_t out_token_stride;
+  int64_t out_head_stride;
+  void* workspace;           /* 16-byte aligned, for this call alone until it has run */
+  int64_t workspace_bytes;   /* at least np_kv_attend_workspace() */
+  int32_t n_heads;           /* query heads: a multiple of n_kv_heads, at most 1024 */
+  int32_t dtype;             /* NP_F32, NP_F16 or NP_BF16 */
+  float scale;               /* > 0 */
+  int32_t window;            /* 0: every key up to the query's position */
+  int32_t sinks;             /* first keys that stay visible under a window */
+} np_kv_attn;
+
+/* Attention of the new tokens of one layer: query head h reads key/value head
+ * h / (n_heads / n_kv_heads); the query at position p sees keys j <= p and,
+ * with window > 0, of those only j > p - window and j < sinks.
+ *   out = sum_j softmax_j(scale * q . k_j) v_j, and 0 where no key is visible.
+ * Sums, maxima and the accumulator are fp32.  Keys in pages that the table
+ * does not name (-1: given back under a window) are not visible. */
+np_status np_kv_attend(const np_kv_desc* kv, int32_t layer, const np_kv_batch* batch, const np_kv_attn* attn,
+                       void* stream);
+
+/* Bytes of workspace that any np_kv_attend on this cache needs; -1 for a
+ * description that the calls would refuse. */
+int64_t np_kv_attend_workspace(const np_kv_desc* kv);
+
+/* Synchronise `stream`, then read and clear the cache's error word:
+ * NP_ERR_OOM (no free page left), NP_ERR_STATE (a row, length, page or token
+ * count out of range), NP_ERR_TIMEOUT (a bounded wait expired) or NP_OK. */
+np_status np_kv_check(const np_kv_desc* kv, void* stream);
+
 /* Number of kernel launches the model has issued since creation. */
 int64_t np_launch_count(np_model* m);
 

@@ -14,6 +14,7 @@ NP_RES_SLOTMAP, NP_RES_WINDOW, NP_RES_FREQUENCY = 0, 1, 2
 NP_PRED_SHARED_ARGMAX, NP_PRED_PERLAYER_SIGMOID = 0, 1
 NP_H2D_STAGED, NP_H2D_FUSED = 0, 1
 NP_SLOTS_REUSE, NP_SLOTS_COMPACT = 0, 1
+NP_KV_PAGE, NP_KV_MAX_BATCH = 64, 1024
 KIND_NAMES = ["dense", "predictor", "set", "gather", "scatter", "ffn", "finish"]
 NP_N_KINDS = len(KIND_NAMES)
 
@@ -51,6 +52,27 @@ class Stats(ctypes.Structure):
                 ("moved_rows", ctypes.c_int64)]
 
 
+class KvDesc(ctypes.Structure):
+    _fields_ = [("n_layers", ctypes.c_int32), ("n_pages", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("max_seqs", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("table", ctypes.c_void_p), ("lengths", ctypes.c_void_p),
+                ("refs", ctypes.c_void_p), ("work", ctypes.c_void_p)]
+
+
+class KvBatch(ctypes.Structure):
+    _fields_ = [("seqs", ctypes.c_void_p), ("cu", ctypes.c_void_p), ("n_seqs", ctypes.c_int32),
+                ("n_tokens", ctypes.c_int32), ("max_tokens", ctypes.c_int32)]
+
+
+class KvAttn(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("out", ctypes.c_void_p), ("q_token_stride", ctypes.c_int64),
+                ("q_head_stride", ctypes.c_int64), ("out_token_stride", ctypes.c_int64),
+                ("out_head_stride", ctypes.c_int64), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_int64), ("n_heads", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("window", ctypes.c_int32), ("sinks", ctypes.c_int32)]
+
+
 # symbol -> (restype, argtypes)
 _P, _I32, _I64, _SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 SIGNATURES = {
@@ -76,6 +98,15 @@ SIGNATURES = {
     "np_host_unregister": (_I32, [_P]),
     "np_ffn_rows_noalloc": (_I32, [_P, _P, _P, _P, _P, _I32, _I32, _I32, _I32, _I32, _P, _P]),
     "np_ffn_rows_noalloc_check": (_I32, [_P]),
+    "np_kv_work_words": (_I64, [_P]),
+    "np_kv_attend_workspace": (_I64, [_P]),
+    "np_kv_reserve": (_I32, [_P, _P, _P, _I32, _P]),
+    "np_kv_fork": (_I32, [_P, _P, _P, _I32, _P]),
+    "np_kv_release": (_I32, [_P, _P, _I32, _I32, _I32, _P]),
+    "np_kv_compact": (_I32, [_P, _P]),
+    "np_kv_append": (_I32, [_P, _I32, _P, _P, _I64, _I64, _P, _I64, _I64, _I32, _P]),
+    "np_kv_attend": (_I32, [_P, _I32, _P, _P, _P]),
+    "np_kv_check": (_I32, [_P, _P]),
     "np_launch_count": (_I64, [_P]),
     "np_status_str": (ctypes.c_char_p, [_I32]),
     "np_last_error": (ctypes.c_char_p, []),

@@ -1,0 +1,797 @@
+// Key/value cache: page operations (reserve, fork, release, compact), the
+// quantising append, and the C entry points of all np_kv_* calls.
+//
+// Page operations work on the block table, the lengths and one count of
+// holders per page, all in device memory, so a decode step needs no
+// round trip to the host and can be captured.  They follow the slot map's
+// rules: the lowest free page first, in list order, so every table is
+// reproducible.  Each is bound by latency (a few kilobytes of tables); only
+// the page copies move real bytes.
+#include <climits>
+#include <cmath>
+
+#include "np.h"
+#include "np_kv.cuh"
+
+namespace np {
+
+namespace {
+
+constexpr int kPageThreads = 1024;
+constexpr int kCopyChunk = 16384;  // bytes one CTA copies at a time
+
+// Layout of np_kv_desc.work, in words.
+struct KvWork {
+  int* err;      // [1] error word
+  int* verdict;  // [1] 1: the running call passed its checks
+  int* n_copies; // [1]
+  int* src;      // [n_list] page copies
+  int* dst;      // [n_list]
+  int* lens;     // [max_seqs] lengths on their way to other rows (fork)
+  int* pages;    // [n_pages] free pages (reserve), renumbering (compact)
+  int* rows;     // [max_seqs][max_pages] table rows on their way (fork)
+};
+
+__host__ __device__ inline long long work_list_words(int n_pages, int max_seqs) {
+  return n_pages / 2 + 1 > max_seqs ? n_pages / 2 + 1 : max_seqs;
+}
+
+__host__ __device__ inline KvWork kv_work(int* w, int n_pages, int max_seqs) {
+  const long long list = work_list_words(n_pages, max_seqs);
+  KvWork k;
+  k.err = w;
+  k.verdict = w + 1;
+  k.n_copies = w + 2;
+  k.src = w + 4;
+  k.dst = k.src + list;
+  k.lens = k.dst + list;
+  k.pages = k.lens + max_seqs;
+  k.rows = k.pages + n_pages;
+  return k;
+}
+
+struct KvPool {
+  int* table;
+  int* lengths;
+  int* refs;
+  int n_pages, max_seqs, max_pages;
+  KvWork w;
+};
+
+// Exclusive prefix sum over the CTA (kPageThreads threads); *total gets the
+// sum.  `red` holds one value per warp.
+__device__ __forceinline__ unsigned long long cta_scan(unsigned long long v, unsigned long long* red,
+                                                       unsigned long long* total) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  unsigned long long x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();
+  if (lane == 31) red[w] = x;
+  __syncthreads();
+  if (w == 0) {
+    unsigned long long t = lane < kPageThreads / 32 ? red[lane] : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long y = __shfl_up_sync(0xffffffffu, t, o);
+      if (lane >= o) t += y;
+    }
+    red[lane] = t;
+  }
+  __syncthreads();
+  const unsigned long long before = w ? red[w - 1] : 0;
+  *total = red[31];
+  return before + x - v;
+}
+
+// ---- reserve -------------------------------------------------------------------
+// One CTA, thread i = listed sequence i.  Checks everything first; then finds
+// the lowest free pages by a scan of the counts and hands them out by prefix
+// sums over what each sequence needs.
+__global__ void __launch_bounds__(kPageThreads, 1) reserve_kernel(const KvPool p, const int* seqs, const int* n_new,
+                                                                  int n) {
+  __shared__ unsigned long long red[32];
+  __shared__ int row_s[kKvMaxBatch], key_s[kKvMaxBatch], base_s[kKvMaxBatch + 1], old_s[kKvMaxBatch];
+  const int i = threadIdx.x;
+  if (i == 0) *p.w.n_copies = 0;
+  if (*p.w.err != 0) return;  // the same for every thread: nothing in this launch has written it yet
+  int row = 0, len = 0, add = 0, page = -1;
+  bool ok = true, writes = false;
+  if (i < n) {
+    row = seqs ? seqs[i] : i;
+    ok = row >= 0 && row < p.max_seqs;
+    if (ok) {
+      len = p.lengths[row];
+      add = n_new[i];
+      ok = len >= 0 && add >= 0 && (long long)len + add <= (long long)p.max_pages * kKvPage;
+    }
+    if (ok && add > 0 && len % kKvPage) {
+      page = p.table[(size_t)row * p.max_pages + len / kKvPage];
+      ok = page >= 0 && page < p.n_pages;
+      writes = ok;
+    }
+    row_s[i] = ok ? row : -1;
+    key_s[i] = writes ? page : -1;
+  }
+  __syncthreads();
+  int rank = 0;
+  if (i < n && ok) {
+    for (int j = 0; j < i; ++j) {
+      ok &= row_s[j] != row;
+      rank += key_s[j] == page;
+    }
+  }
+  const bool copies = i < n && ok && writes && rank < p.refs[page] - 1;
+  const int fresh = i < n && ok ? (len + add + kKvPage - 1) / kKvPage - (len + kKvPage - 1) / kKvPage : 0;
+  if (__syncthreads_or(!ok)) {
+    if (i == 0) *p.w.err = kDevErrBounds;
+    return;
+  }
+  unsigned long long total2;
+  const unsigned long long at2 =
+      cta_scan(((unsigned long long)copies << 40) | (unsigned long long)(fresh + copies), red, &total2);
+  const long long total = (long long)(total2 & 0xffffffffffull);
+  if (total > p.n_pages) {
+    if (i == 0) *p.w.err = kDevErrNoPage;
+    return;
+  }
+  if (i < n) {
+    base_s[i] = (int)(at2 & 0xffffffffffull);
+    old_s[i] = copies ? len / kKvPage : (len + kKvPage - 1) / kKvPage;  // first table slot to fill
+  }
+  if (i == 0) base_s[n] = (int)total;
+  // the `total` lowest free pages
+  long long found = 0;
+  for (long long at = 0; at < p.n_pages && found < total; at += 4 * kPageThreads) {
+    const long long b = at + 4 * i;
+    int c[4];
+    int mine = 0;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      c[t] = b + t < p.n_pages ? p.refs[b + t] : 1;
+      mine += c[t] == 0;
+    }
+    unsigned long long chunk;
+    long long r = found + (long long)cta_scan((unsigned long long)mine, red, &chunk);
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+      if (c[t] == 0) {
+        if (r < total) p.w.pages[r] = (int)(b + t);
+        ++r;
+      }
+    found += (long long)chunk;
+    __syncthreads();
+  }
+  if (found < total) {
+    if (i == 0) *p.w.err = kDevErrNoPage;
+    return;
+  }
+  __syncthreads();
+  for (int r = i; r < (int)total; r += kPageThreads) {
+    int lo = 0, hi = n;  // the last sequence with base <= r that needs a page
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      (base_s[mid] <= r ? lo : hi) = mid;
+    }
+    const int g = p.w.pages[r];
+    p.table[(size_t)row_s[lo] * p.max_pages + old_s[lo] + (r - base_s[lo])] = g;
+    p.refs[g] = 1;
+  }
+  if (copies) {
+    const int c = (int)(at2 >> 40);
+    p.w.src[c] = page;
+    p.w.dst[c] = p.w.pages[base_s[i]];
+    atomicSub(&p.refs[page], 1);
+  }
+  if (i < n) p.lengths[row] = len + add;
+  if (i == 0) *p.w.n_copies = (int)(total2 >> 40);
+}
+
+// ---- page copies ------------------------------------------------------------------
+struct KvCopy {
+  uint8_t* k;
+  uint8_t* v;
+  float* k_scale;
+  float* v_scale;
+  long long side_bytes;  // bytes of one page's keys (or values) of one layer
+  int n_layers, H;
+};
+
+// Copies work.src[c] -> work.dst[c] (keys, values, scales of every layer),
+// then renumbers the table when `remap` is set.  Every CTA takes pieces of
+// 16 KB; 16-byte loads, eight in flight per thread.  Bound by HBM: each byte
+// read and written once.
+__global__ void __launch_bounds__(256) copy_pages_kernel(const KvPool p, const KvCopy c, int remap) {
+  const int n = *p.w.n_copies;
+  const int per_side = (int)((c.side_bytes + kCopyChunk - 1) / kCopyChunk);
+  const long long pieces = (long long)n * c.n_layers * 2 * per_side;
+  const int tid = threadIdx.x;
+  for (long long w = blockIdx.x; w < pieces; w += gridDim.x) {
+    const int piece = (int)(w % per_side);
+    long long t = w / per_side;
+    const int side = (int)(t & 1);
+    t >>= 1;
+    const int layer = (int)(t % c.n_layers), i = (int)(t / c.n_layers);
+    const size_t src = (size_t)layer * p.n_pages + p.w.src[i], dst = (size_t)layer * p.n_pages + p.w.dst[i];
+    uint8_t* base = side ? c.v : c.k;
+    const long long off = (long long)piece * kCopyChunk;
+    const int vecs = (int)((c.side_bytes - off < kCopyChunk ? c.side_bytes - off : kCopyChunk) / 16);
+    const uint4* from = reinterpret_cast<const uint4*>(base + src * c.side_bytes + off);
+    uint4* to = reinterpret_cast<uint4*>(base + dst * c.side_bytes + off);
+    for (int x = tid; x < vecs; x += 256 * 4) {
+      uint4 r[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (x + 256 * u < vecs) r[u] = from[x + 256 * u];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (x + 256 * u < vecs) to[x + 256 * u] = r[u];
+    }
+    if (piece == 0) {
+      float* s = side ? c.v_scale : c.k_scale;
+      for (int h = tid; h < c.H; h += 256) s[dst * c.H + h] = s[src * c.H + h];
+    }
+  }
+  if (remap && n > 0) {
+    const long long entries = (long long)p.max_seqs * p.max_pages;
+    for (long long e = (long long)blockIdx.x * 256 + tid; e < entries; e += (long long)gridDim.x * 256) {
+      const int g = p.table[e];
+      if (g >= 0 && g < p.n_pages) {
+        const int to = p.w.pages[g];
+        if (to != g) p.table[e] = to;
+      }
+    }
+  }
+}
+
+// ---- fork ---------------------------------------------------------------------------
+// Two launches: the first checks (every CTA all of it, so that all agree),
+// takes the source rows aside and moves the counts, the second writes the
+// rows.  Counts are whole numbers, so the order of the atomics is immaterial.
+__global__ void __launch_bounds__(256) fork_take_kernel(const KvPool p, const int* src, const int* dst, int n) {
+  __shared__ int dst_s[kKvMaxBatch];
+  const int tid = threadIdx.x, i = blockIdx.x;
+  bool ok = *p.w.err == 0;
+  for (int j = tid; j < n; j += 256) {
+    const int d = dst[j], s = src[j];
+    dst_s[j] = d;
+    ok &= d >= 0 && d < p.max_seqs && s >= 0 && s < p.max_seqs;
+  }
+  __syncthreads();
+  for (int j = tid; j < n; j += 256)
+    for (int t = 0; t < j; ++t) ok &= dst_s[t] != dst_s[j];
+  const bool bad = __syncthreads_or(!ok) != 0;
+  if (i == 0 && tid == 0) {
+    *p.w.verdict = !bad;
+    if (bad) atomicCAS(p.w.err, 0, kDevErrBounds);
+  }
+  if (bad) return;
+  const int s = src[i], d = dst_s[i];
+  for (int x = tid; x < p.max_pages; x += 256) {
+    const int g = p.table[(size_t)s * p.max_pages + x], old = p.table[(size_t)d * p.max_pages + x];
+    p.w.rows[(size_t)i * p.max_pages + x] = g;
+    if (g >= 0 && g < p.n_pages) atomicAdd(&p.refs[g], 1);
+    if (old >= 0 && old < p.n_pages) atomicSub(&p.refs[old], 1);
+  }
+  if (tid == 0) p.w.lens[i] = p.lengths[s];
+}
+
+__global__ void __launch_bounds__(256) fork_give_kernel(const KvPool p, const int* dst) {
+  if (!*p.w.verdict) return;
+  const int i = blockIdx.x, d = dst[i];
+  for (int x = threadIdx.x; x < p.max_pages; x += 256)
+    p.table[(size_t)d * p.max_pages + x] = p.w.rows[(size_t)i * p.max_pages + x];
+  if (threadIdx.x == 0) p.lengths[d] = p.w.lens[i];
+}
+
+// ---- release ------------------------------------------------------------------------
+// One CTA per listed row; an entry is taken by an exchange, so a row that is
+// listed twice gives its pages up once.
+__global__ void __launch_bounds__(256) release_kernel(const KvPool p, const int* seqs, int window, int sinks) {
+  const int row = seqs ? seqs[blockIdx.x] : (int)blockIdx.x;
+  if (*p.w.err != 0) return;
+  if (row < 0 || row >= p.max_seqs) {
+    if (threadIdx.x == 0) atomicCAS(p.w.err, 0, kDevErrBounds);
+    return;
+  }
+  const long long len = window > 0 ? p.lengths[row] : 0;
+  for (int x = threadIdx.x; x < p.max_pages; x += 256) {
+    const long long first = (long long)x * kKvPage;
+    if (window > 0 && (first + kKvPage - 1 > len - window || first < sinks)) continue;
+    int* e = &p.table[(size_t)row * p.max_pages + x];
+    if (*e < 0) continue;
+    const int g = atomicExch(e, -1);
+    if (g >= 0 && g < p.n_pages) atomicSub(&p.refs[g], 1);
+  }
+  if (window == 0 && threadIdx.x == 0) p.lengths[row] = 0;
+}
+
+// ---- compact ------------------------------------------------------------------------
+// One CTA: counts the pages in use (n), then lists the free pages below n and
+// the used ones from n on, which are equally many, and pairs them in order.
+__global__ void __launch_bounds__(kPageThreads, 1) compact_kernel(const KvPool p) {
+  __shared__ unsigned long long red[32];
+  const int i = threadIdx.x;
+  if (i == 0) *p.w.n_copies = 0;
+  if (*p.w.err != 0) return;
+  unsigned long long mine = 0, live;
+  for (int g = i; g < p.n_pages; g += kPageThreads) mine += p.refs[g] > 0;
+  cta_scan(mine, red, &live);
+  // holes below `live` in the low half of the sum, used pages above in the high half
+  unsigned long long seen = 0;
+  for (long long at = 0; at < p.n_pages; at += kPageThreads) {
+    const long long g = at + i;
+    const bool in = g < p.n_pages;
+    const bool used = in && p.refs[g] > 0;
+    const bool hole = in && !used && g < (long long)live, end = used && g >= (long long)live;
+    unsigned long long chunk;
+    const unsigned long long r =
+        seen + cta_scan((unsigned long long)hole | ((unsigned long long)end << 32), red, &chunk);
+    if (hole) p.w.dst[(int)(r & 0xffffffffu)] = (int)g;
+    if (end) p.w.src[(int)(r >> 32)] = (int)g;
+    if (in) p.w.pages[g] = (int)g;
+    seen += chunk;
+    __syncthreads();
+  }
+  __syncthreads();
+  const int n = (int)(seen >> 32);
+  for (int c = i; c < n; c += kPageThreads) {
+    const int s = p.w.src[c], d = p.w.dst[c];
+    p.w.pages[s] = d;
+    p.refs[d] = p.refs[s];
+    p.refs[s] = 0;
+  }
+  if (i == 0) *p.w.n_copies = n;
+}
+
+// ---- append ---------------------------------------------------------------------------
+// One CTA per (page that gets new tokens, head).  It reads the new tokens'
+// values of that page once into registers, takes the largest magnitude,
+// raises the page's scale if needed, and writes the codes: keys token by
+// token, values through shared memory into the transposed page.  Codes that
+// were there are read again only if the scale changed.
+// Bound by HBM for prompts: 2 (f32: 4) bytes read and 1 written per element.
+constexpr int kAppendThreads = 128;
+
+struct KvAppend {
+  KvView kv;
+  KvBatch batch;
+  const void* k;
+  const void* v;
+  long long k_tok, k_head, v_tok, v_head;
+  int direct;  // no sequence has more than one new token: CTA x = sequence x
+};
+
+// Smallest e in [-40, 40] with amax <= 448 * 2^e (448 = 1.75 * 2^8).
+__device__ __forceinline__ int scale_exponent(float amax) {
+  if (!(amax > 0.f)) return -40;
+  const uint32_t u = __float_as_uint(amax);
+  const int x = (int)(u >> 23) - 127;  // amax = 1.f * 2^x (a denormal only makes x smaller)
+  const int e = x - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return e < -40 ? -40 : e > 40 ? 40 : e;
+}
+
+__device__ __forceinline__ float pow2f(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+// Rescale the codes of a word by a power of two.
+__device__ __forceinline__ uint32_t rescale4(uint32_t w, float r) {
+  const float2 a = f16x2_to_f32x2(e4m3x2_to_f16x2(w & 0xffffu));
+  const float2 b = f16x2_to_f32x2(e4m3x2_to_f16x2(w >> 16));
+  return f32x2_to_e4m3x2(a.x * r, a.y * r) | (f32x2_to_e4m3x2(b.x * r, b.y * r) << 16);
+}
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void load8(const T* src, float* f) {
+  if constexpr (VEC) {
+    constexpr int N = 8 / Elem<T>::E;
+#pragma unroll
+    for (int i = 0; i < N; ++i) Elem<T>::load(reinterpret_cast<const uint4*>(src)[i], f + i * Elem<T>::E);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = kv_to_float<T>(src[i]);
+  }
+}
+
+template <typename T, int D, bool VEC>
+__global__ void __launch_bounds__(kAppendThreads) append_kernel(const KvAppend a) {
+  constexpr int CH = D / 8;                                // chunks of 8 elements per token
+  constexpr int PER = kKvPage * CH / kAppendThreads;       // chunks per thread
+  constexpr int VROW = kKvPage + 4;                        // padded row of the transposed codes
+  __shared__ __align__(16) uint8_t vt[D * VROW];
+  __shared__ float red[kAppendThreads / 32];
+  __shared__ int nan_s[kKvPage];
+  __shared__ int item_s[4];
+  const int tid = threadIdx.x, h = blockIdx.y;
+  if (*a.kv.err != 0) return;
+
+  // which sequence and page
+  KvSeq s;
+  int slot;
+  if (a.direct) {
+    s = kv_seq(a.kv, a.batch, blockIdx.x);
+    if (s.n < 1 || s.n > s.len) return;
+    slot = (s.len - 1) / kKvPage;
+  } else {
+    if (tid == 0) item_s[0] = -1;
+    __syncthreads();
+    // pages touched, summed over the sequences; this CTA is the blockIdx.x-th
+    int before = 0;
+    for (int base = 0; base < a.batch.n_seqs; base += kAppendThreads) {
+      const int i = base + tid;
+      int pages = 0;
+      if (i < a.batch.n_seqs) {
+        const KvSeq t = kv_seq(a.kv, a.batch, i);
+        if (t.n > 0 && t.n <= t.len) pages = (t.len + kKvPage - 1) / kKvPage - (t.len - t.n) / kKvPage;
+      }
+      int x = pages;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if ((tid & 31) >= o) x += y;
+      }
+      __syncthreads();
+      if ((tid & 31) == 31) red[tid >> 5] = __int_as_float(x);
+      __syncthreads();
+      int first = before + x - pages, sum = 0;
+#pragma unroll
+      for (int w = 0; w < kAppendThreads / 32; ++w) {
+        const int t = __float_as_int(red[w]);
+        if (w < (tid >> 5)) first += t;
+        sum += t;
+      }
+      if (pages && (int)blockIdx.x >= first && (int)blockIdx.x < first + pages) {
+        item_s[0] = i;
+        item_s[1] = (int)blockIdx.x - first;
+      }
+      before += sum;
+    }
+    __syncthreads();
+    if (item_s[0] < 0) return;
+    s = kv_seq(a.kv, a.batch, item_s[0]);
+    slot = (s.len - s.n) / kKvPage + item_s[1];
+  }
+  const int start = s.len - s.n;                                     // position of the first new token
+  const int off = start > slot * kKvPage ? start - slot * kKvPage : 0;  // first new token in the page
+  const int end = s.len - slot * kKvPage < kKvPage ? s.len - slot * kKvPage : kKvPage;
+  const int m = end - off;
+  const int tok0 = s.begin + slot * kKvPage + off - start;  // its place in the call's tensors
+  const int page = a.kv.table[(size_t)s.row * a.kv.max_pages + slot];
+  if (page < 0 || page >= a.kv.n_pages || a.kv.refs[page] != 1) {
+    if (tid == 0) atomicExch(a.kv.err, kDevErrBounds);
+    return;
+  }
+  const size_t block = (size_t)page * a.kv.H + h;
+  for (int t = tid; t < kKvPage; t += kAppendThreads) nan_s[t] = 0;
+  __syncthreads();
+
+#pragma unroll 1
+  for (int side = 0; side < 2; ++side) {  // 0: values (their NaNs mark the keys), 1: keys
+    const T* src = side == 0 ? static_cast<const T*>(a.v) + (long long)h * a.v_head + (long long)tok0 * a.v_tok
+                             : static_cast<const T*>(a.k) + (long long)h * a.k_head + (long long)tok0 * a.k_tok;
+    const long long stride = side == 0 ? a.v_tok : a.k_tok;
+    float* scale_p = (side == 0 ? a.kv.v_scale : a.kv.k_scale) + block;
+    uint8_t* codes = (side == 0 ? a.kv.v : a.kv.k) + block * kKvPage * D;
+    float x[PER][8];
+    float top = 0.f;
+#pragma unroll
+    for (int c = 0; c < PER; ++c) {
+      const int t = (c * kAppendThreads + tid) / CH, d = (c * kAppendThreads + tid) % CH * 8;
+      if (t < m) {
+        load8<T, VEC>(src + t * stride + d, x[c]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[c][e]));  // fmaxf passes over a NaN
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    __syncthreads();
+    if ((tid & 31) == 0) red[tid >> 5] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kAppendThreads / 32; ++w) top = fmaxf(top, red[w]);
+    const float need = pow2f(scale_exponent(top));
+    const float had = off > 0 ? *scale_p : 0.f;  // a page's first token starts it afresh
+    const float now = fmaxf(need, had);
+    const bool grown = off > 0 && now != had;
+    const float inv = 1.f / now, ratio = had * inv;
+    __syncthreads();  // everyone has read the old scale
+    if (tid == 0) *scale_p = now;
+#pragma unroll
+    for (int c = 0; c < PER; ++c) {
+      const int t = (c * kAppendThreads + tid) / CH, d = (c * kAppendThreads + tid) % CH * 8;
+      if (t >= m) continue;
+      float* y = x[c];
+      if (side == 0) {
+        bool nan = false;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          nan |= isnan(y[e]);
+          y[e] = isnan(y[e]) ? 0.f : y[e] * inv;
+        }
+        if (nan) nan_s[t] = 1;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] *= inv;
+        if (d == 0 && nan_s[t]) y[0] = __int_as_float(0x7fffffff);
+      }
+      uint2 w;
+      w.x = f32x2_to_e4m3x2(y[0], y[1]) | (f32x2_to_e4m3x2(y[2], y[3]) << 16);
+      w.y = f32x2_to_e4m3x2(y[4], y[5]) | (f32x2_to_e4m3x2(y[6], y[7]) << 16);
+      if (side == 1) {
+        *reinterpret_cast<uint2*>(codes + (off + t) * D + d) = w;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) vt[(d + e) * VROW + off + t] = (uint8_t)((e < 4 ? w.x : w.y) >> (8 * (e & 3)));
+      }
+    }
+    if (side == 1) {
+      if (grown)
+        for (int i = tid; i < off * D / 4; i += kAppendThreads) {
+          uint32_t* p = reinterpret_cast<uint32_t*>(codes) + i;
+          *p = rescale4(*p, ratio);
+        }
+    } else {
+      __syncthreads();
+      // words of 4 tokens: whole new ones are written, others merged with
+      // what is there (rescaled before the first new token if the scale grew)
+      const int w0 = grown ? 0 : off / 4, w1 = (end + 3) / 4;
+      const int nw = w1 - w0;
+      for (int i = tid; i < nw * D; i += kAppendThreads) {
+        const int d = i / nw, w = w0 + i % nw;
+        uint32_t* p = reinterpret_cast<uint32_t*>(codes + d * kKvPage) + w;
+        uint32_t fresh = *reinterpret_cast<const uint32_t*>(vt + d * VROW + 4 * w);
+        if (4 * w < off || 4 * w + 4 > end) {
+          const uint32_t old = *p, scaled = grown ? rescale4(old, ratio) : old;
+          uint32_t r = 0;
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            const int t = 4 * w + b;
+            r |= (t < off ? scaled : t < end ? fresh : old) & (0xffu << (8 * b));
+          }
+          fresh = r;
+        }
+        *p = fresh;
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// ---- host side -------------------------------------------------------------------------
+
+np_status kv_fail(np_status s, const char* what) {
+  set_last_error(what);
+  return s;
+}
+
+bool shape_ok(const np_kv_desc* d) {
+  return d && d->n_layers >= 1 && d->n_pages >= 1 && d->n_pages <= (1 << 28) && d->n_kv_heads >= 1 &&
+         d->n_kv_heads <= 256 && (d->head_dim == 64 || d->head_dim == 128 || d->head_dim == 256) &&
+         d->max_seqs >= 1 && d->max_pages >= 1 && d->max_pages <= INT_MAX / kKvPage &&
+         (long long)d->n_layers * d->n_pages * d->n_kv_heads < (1ll << 31) &&
+         (long long)d->max_seqs * d->max_pages < (1ll << 40);
+}
+
+bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// Every rule np.h states for a description, before any CUDA call.
+np_status check_desc(const np_kv_desc* d, const char* call) {
+  if (!shape_ok(d)) return kv_fail(NP_ERR_ARG, call);
+  if (!d->k || !d->v || !d->k_scale || !d->v_scale || !d->table || !d->lengths || !d->refs || !d->work)
+    return kv_fail(NP_ERR_ARG, call);
+  if (!aligned(d->k, 128) || !aligned(d->v, 128) || !aligned(d->k_scale, 16) || !aligned(d->v_scale, 16) ||
+      !aligned(d->table, 16) || !aligned(d->lengths, 4) || !aligned(d->refs, 16) || !aligned(d->work, 16))
+    return kv_fail(NP_ERR_ARG, call);
+  return NP_OK;
+}
+
+np_status check_batch(const np_kv_desc* d, const np_kv_batch* b, const char* call) {
+  if (!b || b->n_seqs < 1 || b->n_seqs > kKvMaxBatch || b->n_tokens < 0 || b->max_tokens < 0 ||
+      (!b->seqs && b->n_seqs > d->max_seqs) || (!b->cu && b->n_tokens % b->n_seqs))
+    return kv_fail(NP_ERR_ARG, call);
+  if (!aligned(b->seqs, 4) || !aligned(b->cu, 4)) return kv_fail(NP_ERR_ARG, call);
+  if (!b->cu && b->n_tokens / b->n_seqs > b->max_tokens) return kv_fail(NP_ERR_ARG, call);
+  return NP_OK;
+}
+
+KvView view_of(const np_kv_desc* d, int layer) {
+  const size_t blocks = (size_t)layer * d->n_pages * d->n_kv_heads, bytes = (size_t)kKvPage * d->head_dim;
+  KvView v;
+  v.k = static_cast<uint8_t*>(d->k) + blocks * bytes;
+  v.v = static_cast<uint8_t*>(d->v) + blocks * bytes;
+  v.k_scale = d->k_scale + blocks;
+  v.v_scale = d->v_scale + blocks;
+  v.table = d->table;
+  v.lengths = d->lengths;
+  v.refs = d->refs;
+  v.err = d->work;
+  v.n_pages = d->n_pages;
+  v.H = d->n_kv_heads;
+  v.D = d->head_dim;
+  v.max_seqs = d->max_seqs;
+  v.max_pages = d->max_pages;
+  return v;
+}
+
+KvPool pool_of(const np_kv_desc* d) {
+  KvPool p;
+  p.table = d->table;
+  p.lengths = d->lengths;
+  p.refs = d->refs;
+  p.n_pages = d->n_pages;
+  p.max_seqs = d->max_seqs;
+  p.max_pages = d->max_pages;
+  p.w = kv_work(d->work, d->n_pages, d->max_seqs);
+  return p;
+}
+
+KvBatch batch_of(const np_kv_batch* b) { return KvBatch{b->seqs, b->cu, b->n_seqs, b->n_tokens, b->max_tokens}; }
+
+np_status launched(const char* call) {
+  const cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) return NP_OK;
+  return kv_fail(NP_ERR_CUDA, cudaGetErrorString(e));
+}
+
+np_status copy_pages(const np_kv_desc* d, long long most, int remap, cudaStream_t st, const char* call) {
+  KvCopy c{static_cast<uint8_t*>(d->k), static_cast<uint8_t*>(d->v), d->k_scale, d->v_scale,
+           (long long)d->n_kv_heads * kKvPage * d->head_dim, d->n_layers, d->n_kv_heads};
+  long long pieces = most * d->n_layers * 2 * ((c.side_bytes + kCopyChunk - 1) / kCopyChunk);
+  if (pieces < 1) pieces = 1;
+  const unsigned grid = (unsigned)(pieces < 152 * 8 ? pieces : 152 * 8);
+  copy_pages_kernel<<<grid, 256, 0, st>>>(pool_of(d), c, remap);
+  return launched(call);
+}
+
+template <typename T>
+cudaError_t launch_append(const KvAppend& a, int items, bool vec, cudaStream_t st) {
+  const dim3 grid((unsigned)items, (unsigned)a.kv.H);
+  switch (a.kv.D) {
+    case 64:
+      if (vec) append_kernel<T, 64, true><<<grid, kAppendThreads, 0, st>>>(a);
+      else append_kernel<T, 64, false><<<grid, kAppendThreads, 0, st>>>(a);
+      break;
+    case 128:
+      if (vec) append_kernel<T, 128, true><<<grid, kAppendThreads, 0, st>>>(a);
+      else append_kernel<T, 128, false><<<grid, kAppendThreads, 0, st>>>(a);
+      break;
+    default:
+      if (vec) append_kernel<T, 256, true><<<grid, kAppendThreads, 0, st>>>(a);
+      else append_kernel<T, 256, false><<<grid, kAppendThreads, 0, st>>>(a);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+}  // namespace np
+
+using namespace np;
+
+extern "C" int64_t np_kv_work_words(const np_kv_desc* d) {
+  if (!shape_ok(d)) return -1;
+  return 4 + 2 * work_list_words(d->n_pages, d->max_seqs) + d->max_seqs + d->n_pages +
+         (int64_t)d->max_seqs * d->max_pages;
+}
+
+extern "C" int64_t np_kv_attend_workspace(const np_kv_desc* d) {
+  return shape_ok(d) ? (int64_t)kv_attend_workspace(d->head_dim) : -1;
+}
+
+extern "C" np_status np_kv_reserve(const np_kv_desc* d, const int32_t* seqs, const int32_t* n_new, int32_t n,
+                                   void* stream) {
+  const np_status s = check_desc(d, "np_kv_reserve: bad cache description");
+  if (s != NP_OK) return s;
+  if (!n_new || n < 1 || n > kKvMaxBatch || (!seqs && n > d->max_seqs) || !aligned(seqs, 4) || !aligned(n_new, 4))
+    return kv_fail(NP_ERR_ARG, "np_kv_reserve: bad list of sequences");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  reserve_kernel<<<1, kPageThreads, 0, st>>>(pool_of(d), seqs, n_new, n);
+  const np_status l = launched("np_kv_reserve");
+  if (l != NP_OK) return l;
+  return copy_pages(d, n, 0, st, "np_kv_reserve");
+}
+
+extern "C" np_status np_kv_fork(const np_kv_desc* d, const int32_t* src, const int32_t* dst, int32_t n,
+                                void* stream) {
+  const np_status s = check_desc(d, "np_kv_fork: bad cache description");
+  if (s != NP_OK) return s;
+  if (!src || !dst || n < 1 || n > kKvMaxBatch || n > d->max_seqs || !aligned(src, 4) || !aligned(dst, 4))
+    return kv_fail(NP_ERR_ARG, "np_kv_fork: bad list of sequences");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  fork_take_kernel<<<n, 256, 0, st>>>(pool_of(d), src, dst, n);
+  const np_status l = launched("np_kv_fork");
+  if (l != NP_OK) return l;
+  fork_give_kernel<<<n, 256, 0, st>>>(pool_of(d), dst);
+  return launched("np_kv_fork");
+}
+
+extern "C" np_status np_kv_release(const np_kv_desc* d, const int32_t* seqs, int32_t n, int32_t window,
+                                   int32_t sinks, void* stream) {
+  const np_status s = check_desc(d, "np_kv_release: bad cache description");
+  if (s != NP_OK) return s;
+  if (n < 1 || n > kKvMaxBatch || (!seqs && n > d->max_seqs) || window < 0 || sinks < 0 || !aligned(seqs, 4))
+    return kv_fail(NP_ERR_ARG, "np_kv_release: bad list of sequences, window or sinks");
+  release_kernel<<<n, 256, 0, static_cast<cudaStream_t>(stream)>>>(pool_of(d), seqs, window, sinks);
+  return launched("np_kv_release");
+}
+
+extern "C" np_status np_kv_compact(const np_kv_desc* d, void* stream) {
+  const np_status s = check_desc(d, "np_kv_compact: bad cache description");
+  if (s != NP_OK) return s;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  compact_kernel<<<1, kPageThreads, 0, st>>>(pool_of(d));
+  const np_status l = launched("np_kv_compact");
+  if (l != NP_OK) return l;
+  return copy_pages(d, d->n_pages / 2 + 1, 1, st, "np_kv_compact");
+}
+
+extern "C" np_status np_kv_append(const np_kv_desc* d, int32_t layer, const np_kv_batch* b, const void* k,
+                                  int64_t k_tok, int64_t k_head, const void* v, int64_t v_tok, int64_t v_head,
+                                  int32_t dtype, void* stream) {
+  np_status s = check_desc(d, "np_kv_append: bad cache description");
+  if (s == NP_OK) s = check_batch(d, b, "np_kv_append: bad batch");
+  if (s != NP_OK) return s;
+  if (layer < 0 || layer >= d->n_layers || dtype < NP_F32 || dtype > NP_BF16)
+    return kv_fail(NP_ERR_ARG, "np_kv_append: bad layer or dtype");
+  if (b->n_tokens == 0) return NP_OK;
+  const size_t esz = dtype == NP_F32 ? 4 : 2;
+  if (!k || !v || !aligned(k, esz) || !aligned(v, esz) || k_tok < 0 || k_head < 0 || v_tok < 0 || v_head < 0)
+    return kv_fail(NP_ERR_ARG, "np_kv_append: bad tensors");
+  KvAppend a{view_of(d, layer), batch_of(b), k, v, k_tok, k_head, v_tok, v_head, b->max_tokens <= 1 ? 1 : 0};
+  const bool vec = aligned(k, 16) && aligned(v, 16) &&
+                   (((uint64_t)k_tok | (uint64_t)k_head | (uint64_t)v_tok | (uint64_t)v_head) * esz) % 16 == 0;
+  // pages touched by n sequences with N new tokens together: at most
+  // min(N, N / 64 + 2 n)
+  const long long most = (long long)b->n_tokens / kKvPage + 2ll * b->n_seqs;
+  const int items = a.direct ? b->n_seqs : (int)(most < b->n_tokens ? most : b->n_tokens);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = dtype == NP_F32   ? launch_append<float>(a, items, vec, st)
+                        : dtype == NP_F16 ? launch_append<__half>(a, items, vec, st)
+                                          : launch_append<__nv_bfloat16>(a, items, vec, st);
+  return e == cudaSuccess ? NP_OK : kv_fail(NP_ERR_CUDA, cudaGetErrorString(e));
+}
+
+extern "C" np_status np_kv_attend(const np_kv_desc* d, int32_t layer, const np_kv_batch* b, const np_kv_attn* t,
+                                  void* stream) {
+  np_status s = check_desc(d, "np_kv_attend: bad cache description");
+  if (s == NP_OK) s = check_batch(d, b, "np_kv_attend: bad batch");
+  if (s != NP_OK) return s;
+  if (!t || layer < 0 || layer >= d->n_layers || t->dtype < NP_F32 || t->dtype > NP_BF16)
+    return kv_fail(NP_ERR_ARG, "np_kv_attend: bad layer or dtype");
+  if (t->n_heads < 1 || t->n_heads > 1024 || t->n_heads % d->n_kv_heads)
+    return kv_fail(NP_ERR_ARG, "np_kv_attend: n_heads is not a multiple of the cache's heads");
+  if (!std::isfinite(t->scale) || t->scale <= 0.f || t->window < 0 || t->sinks < 0)
+    return kv_fail(NP_ERR_ARG, "np_kv_attend: bad scale, window or sinks");
+  if (b->n_tokens == 0) return NP_OK;
+  const size_t esz = t->dtype == NP_F32 ? 4 : 2;
+  if (!t->q || !t->out || !aligned(t->q, esz) || !aligned(t->out, esz) || t->q_token_stride < 0 ||
+      t->q_head_stride < 0 || t->out_token_stride < 0 || t->out_head_stride < 0)
+    return kv_fail(NP_ERR_ARG, "np_kv_attend: bad tensors");
+  if (!t->workspace || !aligned(t->workspace, 16) ||
+      t->workspace_bytes < (int64_t)kv_attend_workspace(d->head_dim))
+    return kv_fail(NP_ERR_ARG, "np_kv_attend: workspace missing, unaligned or too small");
+  KvAttend a{view_of(d, layer), batch_of(b), t->q, t->out, t->q_token_stride, t->q_head_stride,
+             t->out_token_stride, t->out_head_stride, t->n_heads, t->dtype, t->scale * 1.4426950408889634f,
+             t->window, t->sinks, t->workspace};
+  const cudaError_t e = launch_kv_attend(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? NP_OK : kv_fail(NP_ERR_CUDA, cudaGetErrorString(e));
+}
+
+extern "C" np_status np_kv_check(const np_kv_desc* d, void* stream) {
+  const np_status s = check_desc(d, "np_kv_check: bad cache description");
+  if (s != NP_OK) return s;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  int word = 0;
+  if (cudaMemcpyAsync(&word, d->work, sizeof(int), cudaMemcpyDeviceToHost, st) != cudaSuccess ||
+      cudaStreamSynchronize(st) != cudaSuccess)
+    return kv_fail(NP_ERR_CUDA, "np_kv_check: reading the error word");
+  if (word == 0) return NP_OK;
+  if (cudaMemsetAsync(d->work, 0, sizeof(int), st) != cudaSuccess || cudaStreamSynchronize(st) != cudaSuccess)
+    return kv_fail(NP_ERR_CUDA, "np_kv_check: clearing the error word");
+  if (word == kDevErrNoPage) return kv_fail(NP_ERR_OOM, "key/value cache: no free page left");
+  if (word == kDevErrTimeout) return kv_fail(NP_ERR_TIMEOUT, "key/value cache: a device wait timed out");
+  return kv_fail(NP_ERR_STATE, "key/value cache: a row, page, length or token count was out of range");
+}

@@ -1,0 +1,117 @@
+// Key/value cache: the view of a cache and of a call's sequences that the
+// kernels take, shared by np_kv.cu (pages, append) and the attention kernels.
+#pragma once
+#include "np_common.cuh"
+
+namespace np {
+
+constexpr int kKvPage = 64;        // tokens per page and per scale
+constexpr int kKvMaxBatch = 1024;  // sequences in one call
+
+// Device error codes of the cache's error word (np_kv_check); kDevErrTimeout
+// and kDevErrBounds are shared with the decode path.
+constexpr int kDevErrNoPage = 3;
+
+// One layer of a cache.
+struct KvView {
+  uint8_t* k;      // [n_pages][H][64][D] e4m3
+  uint8_t* v;      // [n_pages][H][D][64] e4m3
+  float* k_scale;  // [n_pages][H]
+  float* v_scale;
+  int* table;      // [max_seqs][max_pages]
+  int* lengths;    // [max_seqs]
+  int* refs;       // [n_pages]
+  int* err;
+  int n_pages, H, D, max_seqs, max_pages;
+};
+
+// The sequences of a call and their new tokens.
+struct KvBatch {
+  const int* seqs;
+  const int* cu;
+  int n_seqs, n_tokens, max_tokens;
+};
+
+struct KvSeq {
+  int row;    // table row
+  int begin;  // first new token in the call's tensors
+  int n;      // new tokens
+  int len;    // tokens held, the new ones included
+};
+
+// Sequence i of a call.  Every number is checked before it is used as an
+// index: a bad one records kDevErrBounds and leaves the sequence without new
+// tokens (n = 0).
+__device__ __forceinline__ KvSeq kv_seq(const KvView& kv, const KvBatch& b, int i) {
+  KvSeq s;
+  s.row = b.seqs ? b.seqs[i] : i;
+  if (b.cu) {
+    s.begin = b.cu[i];
+    s.n = b.cu[i + 1] - s.begin;
+  } else {
+    s.n = b.n_tokens / b.n_seqs;
+    s.begin = i * s.n;
+  }
+  s.len = 0;
+  bool ok = s.row >= 0 && s.row < kv.max_seqs && s.begin >= 0 && s.n >= 0 && s.n <= b.max_tokens &&
+            s.begin <= b.n_tokens - s.n;
+  if (ok) {
+    s.len = kv.lengths[s.row];
+    ok = s.len >= 0 && (s.len + kKvPage - 1) / kKvPage <= kv.max_pages;
+  }
+  if (!ok) {
+    atomicExch(kv.err, kDevErrBounds);
+    s.n = 0;
+    s.len = 0;
+    s.row = 0;
+  }
+  return s;
+}
+
+// Attention of one layer (np_kv_attend).
+struct KvAttend {
+  KvView kv;
+  KvBatch batch;
+  const void* q;
+  void* out;
+  long long q_tok, q_head, o_tok, o_head;  // strides in elements
+  int Hq;
+  int dtype;
+  float scale_log2;  // softmax scale * log2(e)
+  int window, sinks;
+  void* ws;
+};
+size_t kv_attend_workspace(int head_dim);
+cudaError_t launch_kv_attend(const KvAttend& a, cudaStream_t st);
+
+// Generic 16-bit / 32-bit element access.
+template <typename T> __device__ __forceinline__ float kv_to_float(T v);
+template <> __device__ __forceinline__ float kv_to_float<float>(float v) { return v; }
+template <> __device__ __forceinline__ float kv_to_float<__half>(__half v) { return __half2float(v); }
+template <> __device__ __forceinline__ float kv_to_float<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <typename T> __device__ __forceinline__ T kv_from_float(float v);
+template <> __device__ __forceinline__ float kv_from_float<float>(float v) { return v; }
+template <> __device__ __forceinline__ __half kv_from_float<__half>(float v) { return __float2half_rn(v); }
+template <> __device__ __forceinline__ __nv_bfloat16 kv_from_float<__nv_bfloat16>(float v) {
+  return __float2bfloat16_rn(v);
+}
+
+// Two e4m3 codes (low byte first) as two fp16 values: exact, NaN kept.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo;\n\tcvt.u16.u32 lo, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(two));
+  return r;
+}
+
+// Two floats as two e4m3 codes (lo in the low byte), nearest, saturating.
+__device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ float2 f16x2_to_f32x2(uint32_t h) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+}  // namespace np

@@ -1,0 +1,220 @@
+"""Python face of the np_kv_* calls: an 8-bit paged key/value cache.
+
+Argument marshalling only: every operation runs in the CUDA library
+(libnp.so); this module checks tensors and passes pointers, sizes and streams.
+
+One step of a decoding loop over the cache:
+
+    cache.reserve(n_new)                       # once: lengths grow, pages are assigned
+    for layer in range(n_layers):
+        cache.append(layer, k, v)              # the new tokens' keys and values
+        out = cache.attend(layer, q)           # the new tokens' queries
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+
+import torch
+
+from . import _lib as L
+
+PAGE = 64  # tokens per page and per scale (NP_KV_PAGE)
+_DTYPES = {torch.float32: L.NP_F32, torch.float16: L.NP_F16, torch.bfloat16: L.NP_BF16}
+
+
+class KvCache:
+    """Keys and values of `n_layers` layers in e4m3, in pages of 64 tokens with
+    one scale per page and head.  All calls run on torch's current stream of
+    the cache's device.  Calls that change the cache must not overlap on the
+    GPU with other calls on it (one stream, or events between them); `attend`
+    calls may overlap each other.
+
+    Errors that only the device can see (a row, page or length out of range,
+    no free page left) are recorded on the device; until `check()` reports and
+    clears them the calls that change the cache do nothing."""
+
+    def __init__(self, *, n_layers: int, n_pages: int, n_kv_heads: int, head_dim: int, max_seqs: int,
+                 max_pages: int, device: torch.device | int | str | None = None):
+        if min(n_layers, n_pages, n_kv_heads, head_dim, max_seqs, max_pages) < 1:
+            raise ValueError("cache sizes must be positive")
+        dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+
+        def zeros(*shape, dtype):
+            return torch.zeros(shape, dtype=dtype, device=dev)
+
+        self._setup(zeros(n_layers, n_pages, n_kv_heads, PAGE, head_dim, dtype=torch.uint8).view(torch.float8_e4m3fn),
+                    zeros(n_layers, n_pages, n_kv_heads, head_dim, PAGE, dtype=torch.uint8).view(torch.float8_e4m3fn),
+                    zeros(n_layers, n_pages, n_kv_heads, dtype=torch.float32),
+                    zeros(n_layers, n_pages, n_kv_heads, dtype=torch.float32),
+                    torch.full((max_seqs, max_pages), -1, dtype=torch.int32, device=dev),
+                    zeros(max_seqs, dtype=torch.int32), zeros(n_pages, dtype=torch.int32))
+
+    @classmethod
+    def wrap(cls, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
+             table: torch.Tensor, lengths: torch.Tensor, refs: torch.Tensor) -> "KvCache":
+        """A cache over existing device tensors, laid out as np_kv_desc says:
+        k [layers][pages][heads][64][dim] and v [layers][pages][heads][dim][64]
+        float8_e4m3fn, k_scale and v_scale [layers][pages][heads] float32,
+        table [seqs][pages per sequence], lengths [seqs], refs [pages] int32."""
+        self = cls.__new__(cls)
+        self._setup(k, v, k_scale, v_scale, table, lengths, refs)
+        return self
+
+    def _setup(self, k, v, k_scale, v_scale, table, lengths, refs):
+        for t, dt in ((k, torch.float8_e4m3fn), (v, torch.float8_e4m3fn), (k_scale, torch.float32),
+                      (v_scale, torch.float32), (table, torch.int32), (lengths, torch.int32), (refs, torch.int32)):
+            if t.dtype != dt or not t.is_contiguous():
+                raise ValueError(f"cache tensors must be contiguous and of the stated types (wanted {dt})")
+            if not t.is_cuda or t.device != k.device:
+                raise ValueError("cache tensors must be CUDA tensors of one device")
+        if k.dim() != 5 or k.shape[3] != PAGE:
+            raise ValueError(f"k must be [layers][pages][heads][{PAGE}][dim]")
+        n_layers, n_pages, heads, _, dim = k.shape
+        if tuple(v.shape) != (n_layers, n_pages, heads, dim, PAGE):
+            raise ValueError(f"v must be [layers][pages][heads][dim][{PAGE}] of k's sizes")
+        if tuple(k_scale.shape) != (n_layers, n_pages, heads) or k_scale.shape != v_scale.shape:
+            raise ValueError("scales must be [layers][pages][heads]")
+        if table.dim() != 2 or tuple(lengths.shape) != (table.shape[0],) or tuple(refs.shape) != (n_pages,):
+            raise ValueError("table must be [seqs][pages per sequence], lengths [seqs], refs [pages]")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.table, self.lengths, self.refs = table, lengths, refs
+        self.n_layers, self.n_pages, self.n_kv_heads, self.head_dim = n_layers, n_pages, heads, dim
+        self.max_seqs, self.max_pages = table.shape
+        self.device = k.device
+        self.lib = L.load()
+        d = L.KvDesc()
+        d.n_layers, d.n_pages, d.n_kv_heads, d.head_dim = n_layers, n_pages, heads, dim
+        d.max_seqs, d.max_pages = self.max_seqs, self.max_pages
+        words = self.lib.np_kv_work_words(ctypes.byref(d))
+        self._ws_bytes = self.lib.np_kv_attend_workspace(ctypes.byref(d))
+        if words < 0 or self._ws_bytes < 0:
+            raise ValueError("unsupported cache sizes: head_dim must be 64, 128 or 256, at most 256 heads")
+        self._work = torch.zeros(words, dtype=torch.int32, device=self.device)
+        d.k, d.v, d.k_scale, d.v_scale = k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr()
+        d.table, d.lengths, d.refs, d.work = (table.data_ptr(), lengths.data_ptr(), refs.data_ptr(),
+                                              self._work.data_ptr())
+        self.desc = d
+        self._desc = ctypes.byref(d)
+
+    # -- argument checks -----------------------------------------------------
+    def _stream(self) -> int:
+        if torch.cuda.current_device() != self.device.index:
+            raise ValueError(f"the cache lives on {self.device}; make it the current device")
+        return torch.cuda.current_stream().cuda_stream
+
+    def _ints(self, t: torch.Tensor, what: str, n: int | None = None) -> int:
+        if (t.dtype != torch.int32 or t.device != self.device or t.dim() != 1 or not t.is_contiguous()
+                or (n is not None and t.shape[0] != n) or not 1 <= t.shape[0] <= L.NP_KV_MAX_BATCH + 1):
+            raise ValueError(f"{what} must be a contiguous int32 vector on {self.device}"
+                             + ("" if n is None else f" of {n} elements"))
+        return t.data_ptr()
+
+    def _tokens(self, t: torch.Tensor, heads: int | None, what: str):
+        if (t.dim() != 3 or t.shape[2] != self.head_dim or t.dtype not in _DTYPES or t.device != self.device
+                or (heads is not None and t.shape[1] != heads) or (t.stride(2) != 1 and t.numel())):
+            raise ValueError(f"{what} must be [tokens][heads][{self.head_dim}] float32, float16 or bfloat16 on "
+                             f"{self.device}, the last dimension contiguous")
+
+    def _batch(self, n_tokens: int, cu, seqs, max_tokens):
+        if seqs is not None:
+            n = seqs.shape[0]
+            p = self._ints(seqs, "seqs")
+        else:
+            n, p = (self.max_seqs if cu is None else cu.shape[0] - 1), None
+        if cu is not None:
+            c = self._ints(cu, "cu", n + 1)
+            most = n_tokens if max_tokens is None else max_tokens
+        else:
+            if n_tokens % n:
+                raise ValueError(f"{n_tokens} tokens do not divide among {n} sequences: give cu")
+            c, most = None, n_tokens // n
+        return L.KvBatch(p, c, n, n_tokens, most)
+
+    # -- pages ----------------------------------------------------------------
+    def reserve(self, n_new: torch.Tensor, seqs: torch.Tensor | None = None) -> None:
+        """Room for n_new[i] more tokens (int32, on the device) in row seqs[i]
+        (default: row i); lengths grow by n_new, missing pages come from the
+        free ones (lowest first) and a shared page that the new tokens start
+        in is copied.  All or nothing."""
+        st = self._stream()
+        p = self._ints(n_new, "n_new", None if seqs is None else seqs.shape[0])
+        L.check(self.lib.np_kv_reserve(self._desc, None if seqs is None else self._ints(seqs, "seqs"), p,
+                                       n_new.shape[0], st), "np_kv_reserve")
+
+    def fork(self, src: torch.Tensor, dst: torch.Tensor) -> None:
+        """Rows dst[i] become what rows src[i] were, sharing their pages; the
+        dst rows are distinct and may be src rows too (a beam reordering)."""
+        st = self._stream()
+        s, d = self._ints(src, "src"), self._ints(dst, "dst", src.shape[0])
+        L.check(self.lib.np_kv_fork(self._desc, s, d, src.shape[0], st), "np_kv_fork")
+
+    def release(self, seqs: torch.Tensor, window: int = 0, sinks: int = 0) -> None:
+        """Give back the pages of rows `seqs`: all of them, or with window > 0
+        those that no later query sees under that window and sinks."""
+        st = self._stream()
+        L.check(self.lib.np_kv_release(self._desc, self._ints(seqs, "seqs"), seqs.shape[0], window, sinks, st),
+                "np_kv_release")
+
+    def compact(self) -> None:
+        """Pack the used pages into the lowest page numbers."""
+        L.check(self.lib.np_kv_compact(self._desc, self._stream()), "np_kv_compact")
+
+    # -- tokens ---------------------------------------------------------------
+    def append(self, layer: int, k: torch.Tensor, v: torch.Tensor, cu: torch.Tensor | None = None,
+               seqs: torch.Tensor | None = None, max_new: int | None = None) -> None:
+        """Write the new tokens' keys and values of one layer, [tokens][kv
+        heads][dim], sequence after sequence: tokens cu[i]..cu[i+1]-1 belong to
+        row seqs[i] (default: row i).  Without `cu` every sequence has the
+        same number.  `max_new`: no sequence has more (1 selects the
+        single-token launch)."""
+        st = self._stream()
+        self._tokens(k, self.n_kv_heads, "k")
+        self._tokens(v, self.n_kv_heads, "v")
+        if k.shape[0] != v.shape[0] or k.dtype != v.dtype:
+            raise ValueError("k and v must have the same tokens and dtype")
+        b = self._batch(k.shape[0], cu, seqs, max_new)
+        L.check(self.lib.np_kv_append(self._desc, layer, ctypes.byref(b), k.data_ptr(), k.stride(0), k.stride(1),
+                                      v.data_ptr(), v.stride(0), v.stride(1), _DTYPES[k.dtype], st), "np_kv_append")
+
+    def attend(self, layer: int, q: torch.Tensor, cu: torch.Tensor | None = None, seqs: torch.Tensor | None = None,
+               max_q: int | None = None, scale: float | None = None, window: int = 0, sinks: int = 0,
+               out: torch.Tensor | None = None) -> torch.Tensor:
+        """Attention of the new tokens' queries, [tokens][heads][dim], over one
+        layer of the cache: causal, with window > 0 only the last `window` keys
+        and the first `sinks`.  Query heads share key heads in groups of
+        heads / kv heads.  `scale` defaults to 1/sqrt(dim).  Returns `out`
+        (default: a new tensor like q); rows of no sequence are left alone."""
+        st = self._stream()
+        self._tokens(q, None, "q")
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        else:
+            self._tokens(out, q.shape[1], "out")
+            if out.shape[0] != q.shape[0] or out.dtype != q.dtype:
+                raise ValueError("out must have q's shape and dtype")
+            if q.numel() and _spans_overlap(q, out):
+                raise ValueError("out may not share memory with q")
+        b = self._batch(q.shape[0], cu, seqs, max_q)
+        ws = torch.empty(self._ws_bytes, dtype=torch.uint8, device=q.device)
+        t = L.KvAttn(q.data_ptr(), out.data_ptr(), q.stride(0), q.stride(1), out.stride(0), out.stride(1),
+                     ws.data_ptr(), self._ws_bytes, q.shape[1], _DTYPES[q.dtype],
+                     1.0 / math.sqrt(self.head_dim) if scale is None else scale, window, sinks)
+        L.check(self.lib.np_kv_attend(self._desc, layer, ctypes.byref(b), ctypes.byref(t), st), "np_kv_attend")
+        return out
+
+    def check(self) -> None:
+        """Synchronise the current stream and raise NpError if a call recorded
+        an error (status -2: no free page left; -6: a row, page, length or
+        token count out of range; -5: an expired wait); clears it."""
+        L.check(self.lib.np_kv_check(self._desc, self._stream()), "np_kv_check")
+
+
+def _spans_overlap(a: torch.Tensor, b: torch.Tensor) -> bool:
+    """The byte ranges from first to last element of two tensors overlap."""
+    def span(t):
+        last = sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
+        return t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size()
+    a0, a1 = span(a)
+    b0, b1 = span(b)
+    return a0 < b1 and b0 < a1

@@ -1,0 +1,585 @@
+"""The key/value cache on the GPU against the 64-bit oracle: page operations
+and codes exactly, attention within a bound derived from the arithmetic.
+
+The bound, per output element: half a step of the output type relative to the
+value; plus, times sum_j p_j |v_j|,
+  * 2 dz, dz the error of a logit: D fp32 products and sums (2^-23 each, so
+    that a truncating adder is covered), the scale factors, and the split of
+    q into fp16 parts (2^-11 relative to q for 16-bit types, whose parts are
+    exact down to the subnormals, 2^-21 for fp32), all times
+    max_j scale sum_d |q_d k_jd|;
+  * the rounding of the weights: 2^-11 (fp16) for 16-bit outputs, 2^-21 for
+    fp32 (two parts);
+  * (n + 16) 2^-23 for sums over n keys and the exponential;
+plus n 2^-31 max|v| for weights below fp16's normal range."""
+import numpy as np
+import pytest
+import torch
+
+from oracle.kv import PAGE, KvOracle
+
+pytestmark = pytest.mark.gpu
+
+DT = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from sparse_activation_decode_gb300.build import build
+    build()
+
+
+def i32(x):
+    return torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")
+
+
+def cu_of(counts):
+    return i32(np.concatenate([[0], np.cumsum(counts)]))
+
+
+class Pair:
+    """A cache and its oracle, driven by the same calls."""
+
+    def __init__(self, L=1, P=32, H=2, D=64, B=4, W=8, seed=0):
+        from sparse_activation_decode_gb300 import KvCache
+        self.c = KvCache(n_layers=L, n_pages=P, n_kv_heads=H, head_dim=D, max_seqs=B, max_pages=W)
+        self.o = KvOracle(L, P, H, D, B, W)
+        self.rng = np.random.default_rng(seed)
+        self.L, self.H, self.D = L, H, D
+
+    def reserve(self, n_new, seqs=None):
+        self.c.reserve(i32(n_new), None if seqs is None else i32(seqs))
+        self.o.reserve(n_new, seqs)
+
+    def fork(self, src, dst):
+        self.c.fork(i32(src), i32(dst))
+        self.o.fork(src, dst)
+
+    def release(self, seqs, window=0, sinks=0):
+        self.c.release(i32(seqs), window, sinks)
+        self.o.release(seqs, window, sinks)
+
+    def compact(self):
+        self.c.compact()
+        self.o.compact()
+
+    def tokens(self, n, dtype, gain=1.0):
+        x = self.rng.standard_normal((n, self.H, self.D)) * np.exp(self.rng.standard_normal((self.H, self.D))) * gain
+        return torch.from_numpy(x).to(DT[dtype]).cuda()
+
+    def append(self, counts, dtype="f32", seqs=None, gain=1.0, layer=0, max_new=None):
+        k, v = self.tokens(sum(counts), dtype, gain), self.tokens(sum(counts), dtype, gain)
+        self.put(k, v, counts, seqs, layer, max_new)
+
+    def put(self, k, v, counts, seqs=None, layer=0, max_new=None):
+        self.c.append(layer, k, v, cu=cu_of(counts), seqs=None if seqs is None else i32(seqs), max_new=max_new)
+        self.o.append(layer, k.double().cpu().numpy(), v.double().cpu().numpy(), counts, seqs)
+
+    def grow(self, counts, dtype="f32", seqs=None, gain=1.0):
+        self.reserve(counts, seqs)
+        for layer in range(self.L):
+            self.append(counts, dtype, seqs, gain, layer)
+
+    def same(self):
+        self.c.check()
+        o, c = self.o, self.c
+        assert np.array_equal(c.table.cpu().numpy(), o.table)
+        assert np.array_equal(c.refs.cpu().numpy(), o.refs)
+        assert np.array_equal(c.lengths.cpu().numpy(), o.len)
+        held = np.nonzero(o.refs)[0]
+        assert np.array_equal(c.k_scale.cpu().numpy()[:, held], o.ks[:, held])
+        assert np.array_equal(c.v_scale.cpu().numpy()[:, held], o.vs[:, held])
+        # codes of the tokens held (what lies behind a sequence's end is not looked at)
+        k, v = c.k.float().cpu().numpy().astype(np.float64), c.v.float().cpu().numpy().astype(np.float64)
+        for row in range(o.table.shape[0]):
+            for s in range(-(-int(o.len[row]) // PAGE)):
+                p, m = o.table[row, s], min(PAGE, int(o.len[row]) - s * PAGE)
+                if p >= 0:
+                    assert np.array_equal(k[:, p, :, :m], o.k[:, p, :, :m], equal_nan=True)
+                    assert np.array_equal(v[:, p, :, :, :m], o.v[:, p, :, :, :m])
+
+    def query(self, counts, heads, dtype, gain=1.0):
+        return torch.from_numpy(self.rng.standard_normal((sum(counts), heads, self.D)) * gain).to(DT[dtype]).cuda()
+
+    def attend_close(self, counts, heads, dtype, window=0, sinks=0, seqs=None, gain=1.0, q=None, layer=0, scale=None,
+                     **kw):
+        q = self.query(counts, heads, dtype, gain) if q is None else q
+        got = self.c.attend(layer, q, cu=cu_of(counts), seqs=None if seqs is None else i32(seqs), window=window,
+                            sinks=sinks, scale=scale, **kw)
+        self.c.check()
+        close(self.o, layer, q, counts, got, dtype, window, sinks, seqs, scale)
+        return got
+
+
+def close(o, layer, q, counts, got, dtype, window=0, sinks=0, seqs=None, scale=None):
+    scale = 1 / np.sqrt(o.D) if scale is None else scale
+    ref, mag, reach = o.attend(layer, q.double().cpu().numpy(), counts, scale, window, sinks, seqs)
+    n, z, vmax = reach[..., 0:1], reach[..., 1:2], reach[..., 2:3]
+    t = DT[dtype]
+    wide = dtype == "f32"
+    dz = ((o.D + 16) * 2.0 ** -23 + (2.0 ** -21 if wide else 2.0 ** -24)) * z
+    tol = (2 * dz + (2.0 ** -21 if wide else 2.0 ** -11) + (n + 16) * 2.0 ** -23) * mag + n * 2.0 ** -31 * vmax
+    tol = tol + torch.finfo(t).eps / 2 * (np.abs(ref) + tol) + torch.finfo(t).tiny * 2.0 ** -8
+    y = got.double().cpu().numpy()
+    bad = np.isnan(y) != np.isnan(ref)
+    # every value within tol of ref is a right result before the rounding to
+    # the type, and IEEE 754 rounds those beyond its largest value to infinity
+    over = np.abs(ref) + tol > float(torch.finfo(t).max)
+    y = np.where(over & (y == np.copysign(np.inf, ref)), ref, y)
+    off = np.abs(y - ref) > tol
+    assert not bad.any(), np.argwhere(bad)[:5]
+    assert not off.any(), (np.argwhere(off)[:5], np.max(np.where(off, np.abs(y - ref) / tol, 0)))
+
+
+# ---- pages -------------------------------------------------------------------
+def test_a_search_with_forks_copies_release_and_compaction():
+    for seed in range(3):
+        p = Pair(L=2, P=40, H=2, D=64, B=6, W=7, seed=seed)
+        p.grow([70, 1, 64, 0, 130, 63])
+        p.same()
+        p.fork([0, 0, 4, 2, 4, 4], [0, 1, 2, 3, 4, 5])
+        p.same()
+        for _ in range(3):
+            p.grow([1] * 6)
+            p.same()
+        p.release([1, 1, 4])                         # a row listed twice gives its pages up once
+        p.same()
+        p.grow([40, 3], seqs=[5, 1])
+        p.release([5, 2], window=20, sinks=1)
+        p.same()
+        p.compact()
+        p.same()
+        p.compact()
+        p.grow([65, 1, 1], seqs=[4, 3, 0])
+        p.same()
+        p.attend_close([3, 1], 4, "f32", seqs=[5, 2], window=20, sinks=1)
+
+
+def test_reserve_takes_all_or_nothing():
+    from sparse_activation_decode_gb300 import NpError
+    p = Pair(P=4, B=3, W=3)
+    p.grow([100, 10, 0])
+    for bad, status in (([65, 0, 65], -2), ([0, 0, 200], -6), ([0, -1, 0], -6)):
+        p.c.reserve(i32(bad))
+        with pytest.raises(NpError) as e:
+            p.c.check()
+        assert e.value.status == status
+        p.same()
+    for seqs in ([0, 0], [0, 3], [-1, 1]):
+        p.c.reserve(i32([1, 1]), i32(seqs))
+        with pytest.raises(NpError) as e:
+            p.c.check()
+        assert e.value.status == -6
+        p.same()
+    p.c.fork(i32([0, 0]), i32([1, 1]))
+    with pytest.raises(NpError):
+        p.c.check()
+    p.c.fork(i32([0, 7]), i32([1, 2]))
+    with pytest.raises(NpError):
+        p.c.check()
+    p.same()
+    p.grow([28, 54, 0])                              # exactly the free room of the last pages
+    p.same()
+
+
+def test_while_an_error_stands_nothing_changes():
+    from sparse_activation_decode_gb300 import NpError
+    p = Pair(P=2, B=2, W=2)
+    p.grow([64, 3])
+    k = p.c.k.clone()
+    p.c.reserve(i32([1, 0]))                          # no page left
+    p.c.append(0, p.tokens(1, "f32"), p.tokens(1, "f32"), cu=i32([0, 1, 1]))
+    p.c.release(i32([1]))
+    p.c.compact()
+    p.c.fork(i32([0]), i32([1]))
+    with pytest.raises(NpError):
+        p.c.check()
+    assert torch.equal(k.view(torch.uint8), p.c.k.view(torch.uint8))
+    p.same()
+    p.release([1])
+    p.grow([1, 0])
+    p.same()
+
+
+@pytest.mark.parametrize("n_pages", [3, 1000, 5000])
+def test_compact_and_reserve_over_larger_pools(n_pages):
+    rng = np.random.default_rng(n_pages)
+    p = Pair(P=n_pages, H=1, D=64, B=3, W=max(1, n_pages // 3))
+    room = max(1, n_pages // 3) * PAGE
+    p.reserve([room, room // 2, room - 1])
+    keep = [s for s in range(3) if rng.random() < 0.7] or [1]
+    p.c.k.view(torch.uint8).copy_(torch.randint(0, 120, p.c.k.shape, device="cuda", dtype=torch.uint8))
+    p.o.k[:] = p.c.k.float().cpu().numpy()
+    p.c.v.view(torch.uint8).copy_(torch.randint(0, 120, p.c.v.shape, device="cuda", dtype=torch.uint8))
+    p.o.v[:] = p.c.v.float().cpu().numpy()
+    p.release([s for s in range(3) if s not in keep] + [0])
+    p.release(keep, window=room // 3, sinks=70)
+    p.compact()
+    p.same()
+    p.reserve([5, 0, 0])
+    p.same()
+
+
+# ---- append --------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_append_codes_are_exact(dtype, D):
+    p = Pair(L=2, P=24, H=3, D=D, B=4, W=6, seed=D)
+    p.grow([1, 63, 64, 65], dtype)
+    p.same()
+    p.grow([70, 0, 1, 3], dtype, gain=30.0)           # scales grow: earlier codes are rescaled
+    p.same()
+    p.reserve([1, 1, 1, 1])
+    p.append([1, 1, 1, 1], dtype, gain=100.0, layer=1, max_new=1)
+    p.append([1, 1, 1, 1], dtype, gain=1e-3, layer=0, max_new=1)
+    p.same()
+    p.grow([2, 5], dtype, seqs=[3, 0], gain=1e4)
+    p.same()
+
+
+def test_append_extremes():
+    p = Pair(P=8, H=1, D=64, B=1, W=8)
+    p.reserve([64 * 4])
+    x = np.zeros((256, 1, 64), dtype=np.float32)
+    x[0, 0, 0] = np.inf
+    x[1, 0, 1] = -3e38
+    x[64, 0, 3] = 1e-38                               # the smallest scale; everything rounds to zero
+    x[65, 0, 3] = 1e-41
+    x[128, 0, 5] = 448.0
+    x[129, 0, 5] = np.nextafter(np.float32(448.0), np.float32(1e9))
+    x[192] = 2.0 ** -9
+    x[193] = 1000.0
+    y = x.copy()
+    x[70, 0, 9] = np.nan
+    y[71, 0, 9] = np.nan
+    p.put(torch.from_numpy(x).cuda(), torch.from_numpy(y).cuda(), [256])
+    p.same()
+
+
+def test_append_strides_and_padding():
+    p = Pair(P=12, H=2, D=64, B=3, W=4)
+    p.reserve([5, 70, 1])
+    counts = [5, 70, 1]
+    buf = torch.randn(90, 7 * 64 + 1, device="cuda")            # rows of 449 floats: nothing is 16-byte aligned
+    k = buf.as_strided((90, 2, 64), (449, 64, 1), 1)
+    v = buf.as_strided((90, 2, 64), (449, 128, 1), 130)
+    p.c.append(0, k, v, cu=cu_of(counts))                        # 14 tokens behind the last sequence
+    p.o.append(0, k[:76].double().cpu().numpy(), v[:76].double().cpu().numpy(), counts)
+    p.same()
+    qkv = torch.randn(76, 10, 64, device="cuda", dtype=torch.float16)
+    p.put(qkv[:, 6:8], qkv[:, 8:10], counts)
+    p.same()
+    p.attend_close(counts, 6, "f16", q=qkv[:, 0:6])
+
+
+def test_append_refuses_shared_and_missing_pages():
+    from sparse_activation_decode_gb300 import NpError
+    p = Pair(P=6, B=3, W=3)
+    p.grow([10, 5, 0])
+    p.fork([0], [2])
+    k = p.c.k.clone()
+    one = p.tokens(1, "f32")
+    p.c.append(0, one, one, cu=i32([0, 1]), seqs=i32([2]))       # not reserved: the page is shared
+    with pytest.raises(NpError):
+        p.c.check()
+    p.c.append(0, p.tokens(7, "f32"), p.tokens(7, "f32"), cu=i32([0, 7]), seqs=i32([1]))   # 7 tokens of a length of 5
+    p.c.append(0, one, one, cu=i32([0, 1]), seqs=i32([3]))
+    with pytest.raises(NpError):
+        p.c.check()
+    for cu in ([0, 2], [1, 0], [-1, 1], [0, 1 << 30]):
+        p.c.append(0, one, one, cu=i32(cu), seqs=i32([1]))
+        with pytest.raises(NpError):
+            p.c.check()
+    p.c.table[1, 0] = 99
+    p.c.append(0, one, one, cu=i32([0, 1]), seqs=i32([1]))
+    with pytest.raises(NpError):
+        p.c.check()
+    assert torch.equal(k.view(torch.uint8), p.c.k.view(torch.uint8))
+
+
+# ---- attention -------------------------------------------------------------------
+SHAPES = [(64, 1, 1), (64, 2, 6), (128, 2, 2), (128, 1, 8), (128, 2, 10), (256, 1, 4), (256, 2, 2)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("D,H,heads", SHAPES)
+def test_single_tokens(dtype, D, H, heads):
+    p = Pair(P=60, H=H, D=D, B=6, W=40, seed=D + heads)
+    lens = [1, 2, 63, 64, 65, 1500]
+    p.grow(lens)
+    p.attend_close([1] * 6, heads, dtype, max_q=1)
+    p.attend_close([1] * 6, heads, dtype, window=37, sinks=3, max_q=1)
+    p.attend_close([1, 1], heads, dtype, window=1, sinks=0, seqs=[5, 3], max_q=1)
+    p.attend_close([1, 0, 1], heads, dtype, window=700, sinks=130, seqs=[5, 1, 4], gain=6.0)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("D,H,heads", SHAPES)
+def test_prompts(dtype, D, H, heads):
+    p = Pair(P=40, H=H, D=D, B=5, W=12, seed=D * heads)
+    p.grow([600, 129, 64, 3, 200], dtype if dtype != "f32" else "f16")
+    p.attend_close([70, 129, 1, 3, 33], heads, dtype)
+    p.attend_close([300, 17], heads, dtype, window=50, sinks=5, seqs=[0, 4])
+    p.attend_close([600, 0, 2], heads, dtype, window=64, sinks=64, seqs=[0, 2, 3], max_q=600)
+    p.attend_close([5, 9], heads, dtype, seqs=[1, 4], gain=8.0)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "f32"])
+def test_rows_that_see_nothing_are_zero(dtype):
+    p = Pair(P=10, H=1, D=128, B=4, W=4)
+    p.grow([0, 2, 130, 66])
+    got = p.attend_close([3, 5, 1, 67], 4, dtype)     # queries before the first key
+    assert torch.count_nonzero(got[:6]).item() == 0 and torch.count_nonzero(got[6]).item() > 0
+    p.release([2], window=1, sinks=0)                 # both full pages of 130 tokens go; the last one stays
+    p.attend_close([1, 40], 4, dtype, seqs=[2, 1])
+    p.release([3], window=1)
+    p.c.table[3, :] = -1
+    p.o.table[3, :] = -1
+    got = p.attend_close([9, 20], 4, dtype, seqs=[3, 2])
+    assert torch.count_nonzero(got[:9]).item() == 0
+
+
+def test_rows_of_no_sequence_are_left_alone_and_strides_hold():
+    p = Pair(P=12, H=2, D=64, B=3, W=6)
+    p.grow([100, 30, 64])
+    for counts, mq in (([1, 1, 1], 1), ([40, 5, 64], None)):
+        n = sum(counts)
+        for dtype in ("f16", "f32"):
+            q = torch.randn(n + 9, 4 * 64 + 1, device="cuda", dtype=DT[dtype]).as_strided((n + 9, 4, 64),
+                                                                                       (257, 64, 1), 1)
+            out = torch.full((n + 9, 4 * 64 + 3), 7.0, device="cuda", dtype=DT[dtype]).as_strided(
+                (n + 9, 4, 64), (259, 64, 1), 3)
+            got = p.c.attend(0, q, cu=cu_of(counts), max_q=mq, out=out)
+            p.c.check()
+            assert got is out and (out[n:] == 7.0).all()
+            close(p.o, 0, q[:n], counts, out[:n], dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("counts", [[1, 1], [80, 45]], ids=["single", "prompt"])
+def test_nan_and_infinity_in_masked_places_do_not_leak(dtype, counts):
+    p = Pair(P=16, H=1, D=64, B=2, W=6)
+    # every byte of the pool is a NaN before the tokens come: what lies behind
+    # the end of a sequence is never looked at
+    p.c.k.view(torch.uint8).fill_(0x7f)
+    p.c.v.view(torch.uint8).fill_(0xff)
+    p.c.k_scale.fill_(float("nan"))
+    p.c.v_scale.fill_(float("nan"))
+    p.reserve([330, 101])
+    k, v = p.tokens(431, "f32"), p.tokens(431, "f32")
+    k[100, 0, 5] = float("nan")
+    v[101, 0, 6] = float("nan")
+    v[102, 0, 7] = float("inf")
+    p.put(k, v, [330, 101])
+    got = p.attend_close(counts, 2, dtype, window=100, sinks=4)
+    assert torch.isfinite(got.float()).all()
+    if counts[0] > 1:
+        # queries from position 300 on see key 201 on under this window; those
+        # at 250.. see the keys from 101 on: some rows are NaN, others are not
+        got = p.attend_close(counts, 2, dtype, window=150)
+        gone = torch.isnan(got.float()).all(-1).all(-1)
+        assert gone.sum().item() == 1 and not torch.isnan(got[2:].float()).any()
+
+
+@pytest.mark.parametrize("counts", [[1, 1], [20, 30]], ids=["single", "prompt"])
+def test_nan_in_a_query_stays_in_its_row(counts):
+    p = Pair(P=16, H=1, D=128, B=2, W=6)
+    p.grow([330, 101])
+    for dtype in ("f16", "bf16", "f32"):
+        q = p.query(counts, 4, dtype)
+        q[0, 1, 3] = float("nan")
+        q[1, 2, 4] = float("inf")
+        got = p.c.attend(0, q, cu=cu_of(counts))
+        p.c.check()
+        bad = torch.isnan(got.float()).any(-1)
+        assert bad[0, 1] and torch.isnan(got[0, 1].float()).all() and bad[1, 2]
+        bad[0, 1] = bad[1, 2] = False
+        assert not bad.any()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "f32"])
+def test_scales_far_apart(dtype):
+    # pages whose values differ by many powers of two, in either order, and
+    # queries that attend sharply to one of them
+    p = Pair(P=16, H=1, D=64, B=2, W=8)
+    p.reserve([5 * 64, 5 * 64])
+    k, v = torch.randn(640, 1, 64, device="cuda"), torch.randn(640, 1, 64, device="cuda")
+    for i, e in enumerate([20, -20, 0, 30, -30, -35, 25, 3, -10, 12]):
+        v[64 * i:64 * i + 64] *= 2.0 ** e
+        k[64 * i:64 * i + 64] *= 2.0 ** (e / 16)
+    p.put(k, v, [320, 320])
+    for gain in (0.1, 1.0, 20.0):
+        p.attend_close([1, 1], 4, dtype, gain=gain)
+        p.attend_close([90, 70], 4, dtype, gain=gain)
+        q = p.query([1, 1], 4, dtype)
+        q[:] = (k[[70, 400]] * 4).to(q.dtype)
+        p.attend_close([1, 1], 4, dtype, q=q)
+
+
+def test_large_and_small_queries():
+    p = Pair(P=16, H=1, D=128, B=2, W=8)
+    p.grow([200, 300])
+    for counts in ([1, 1], [40, 60]):
+        for dtype, gain, scale in (("f32", 1e30, 1e-31), ("bf16", 1e30, 1e-31), ("f32", 1e-30, 1e29),
+                                   ("bf16", 1e-30, 1e29), ("f16", 1e4, 1e-5), ("f16", 1e-6, 1e4)):
+            p.attend_close(counts, 2, dtype, gain=gain, scale=scale)
+        q = p.query(counts, 2, "f32")
+        q[..., 64:] *= 1e-12                              # elements far below the row's largest
+        p.attend_close(counts, 2, "f32", q=q)
+        p.attend_close(counts, 2, "f32", q=torch.zeros_like(q))
+
+
+def test_long_caches_and_many_splits():
+    p = Pair(P=420, H=2, D=64, B=3, W=400)
+    p.reserve([20000, 3, 6400])
+    k, v = torch.randn(26403, 2, 64, device="cuda"), torch.randn(26403, 2, 64, device="cuda")
+    p.put(k, v, [20000, 3, 6400])
+    p.same()
+    for dtype in ("f32", "bf16"):
+        p.attend_close([1, 1, 1], 8, dtype, max_q=1)
+        p.attend_close([2, 2, 5], 2, dtype)
+        p.attend_close([1, 1, 1], 2, dtype, window=9000, sinks=100)
+
+
+def test_many_sequences():
+    p = Pair(P=600, H=1, D=64, B=300, W=3)
+    counts = [int(x) for x in np.random.default_rng(0).integers(0, 100, 300)]
+    p.grow(counts, "bf16")
+    p.same()
+    p.attend_close([min(c, 2) for c in counts], 2, "bf16")
+    order = np.random.default_rng(1).permutation(300)[:200].tolist()
+    p.attend_close([min(counts[i], 1) for i in order], 2, "f32", seqs=order, max_q=1)
+
+
+def test_bad_numbers_on_the_device_are_recorded():
+    from sparse_activation_decode_gb300 import NpError
+    p = Pair(P=6, B=2, W=3)
+    p.grow([100, 30])
+    q = p.query([1, 1], 2, "f16")
+
+    def bad(**kw):
+        out = torch.full_like(q, 3.0)
+        p.c.attend(0, q, out=out, **kw)
+        with pytest.raises(NpError) as e:
+            p.c.check()
+        assert e.value.status == -6
+        return out
+    for seqs in ([0, 2], [-1, 0]):
+        bad(cu=i32([0, 1, 2]), seqs=i32(seqs))
+    for cu in ([0, 1, 3], [0, 2, 1], [-5, 1, 2]):
+        bad(cu=i32(cu))
+    bad(cu=i32([0, 2, 2]), max_q=1)
+    p.c.lengths[1] = 1000
+    bad(cu=i32([0, 1, 2]))
+    p.c.lengths[1] = 30
+    for page in (6, 1 << 30, -7):
+        p.c.table[0, 1] = page
+        bad(cu=i32([0, 1, 2]))
+    p.c.table[0, 1] = 1
+
+
+# ---- how calls are made ---------------------------------------------------------
+def test_wrapper_refuses_misuse():
+    from sparse_activation_decode_gb300 import KvCache, NpError
+    p = Pair(P=6, H=2, D=64, B=2, W=3)
+    p.grow([10, 10])
+    c, q, kv = p.c, p.query([1, 1], 4, "f16"), p.tokens(2, "f16")
+    for f in (lambda: c.attend(0, q.cpu()), lambda: c.attend(0, q[..., :32]), lambda: c.attend(0, q.double()),
+              lambda: c.attend(0, q.transpose(1, 2)), lambda: c.attend(0, q, out=q),
+              lambda: c.attend(0, q, out=torch.empty_like(q).float()), lambda: c.attend(0, q[:1], cu=None),
+              lambda: c.attend(0, q, cu=torch.tensor([0, 1, 2])), lambda: c.attend(0, q, cu=i32([0, 2]).long()),
+              lambda: c.append(0, kv, kv[:1]), lambda: c.append(0, kv, kv.float()), lambda: c.append(0, q, q),
+              lambda: c.reserve(i32([[1, 1]])), lambda: c.fork(i32([0]), i32([0, 1])),
+              lambda: KvCache(n_layers=1, n_pages=2, n_kv_heads=1, head_dim=80, max_seqs=1, max_pages=1),
+              lambda: KvCache.wrap(c.k, c.v, c.k_scale, c.v_scale, c.table, c.lengths, c.refs[:3])):
+        with pytest.raises(ValueError):
+            f()
+    for f in (lambda: c.attend(1, q), lambda: c.attend(0, q[:, :3].contiguous()), lambda: c.attend(0, q, scale=-1.0),
+              lambda: c.attend(0, q, window=-1), lambda: c.append(5, kv, kv), lambda: c.release(i32([0]), window=-3)):
+        with pytest.raises(NpError):
+            f()
+    p.same()
+
+
+def test_a_step_is_captured_and_replayed_on_another_stream():
+    p = Pair(L=2, P=40, H=2, D=64, B=3, W=8)
+    p.grow([62, 100, 5])
+    side = torch.cuda.Stream()
+    one = i32([1, 1, 0])
+    cu = i32([0, 1, 2, 2])
+    k = [torch.zeros(3, 2, 64, device="cuda", dtype=torch.bfloat16) for _ in range(4)]
+    q = torch.zeros(3, 4, 64, device="cuda", dtype=torch.bfloat16)
+    outs = [torch.full_like(q, 9.0) for _ in range(2)]
+
+    def step():
+        p.c.reserve(one)
+        for layer in range(2):
+            p.c.append(layer, k[2 * layer], k[2 * layer + 1], cu=cu, max_new=1)
+            p.c.attend(layer, q, cu=cu, max_q=1, out=outs[layer])
+
+    graphs = []
+    torch.cuda.synchronize()
+    for _ in range(2):                                 # two graphs of the same step: each with its own workspace
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            step()
+        graphs.append(g)
+    for i in range(5):
+        for t in k + [q]:
+            t.copy_(torch.from_numpy(p.rng.standard_normal(tuple(t.shape))))
+        with torch.cuda.stream(side):
+            side.wait_stream(torch.cuda.default_stream())
+            graphs[i % 2].replay()
+        torch.cuda.default_stream().wait_stream(side)
+        p.o.reserve([1, 1, 0])
+        for layer in range(2):
+            p.o.append(layer, k[2 * layer][:2].double().cpu().numpy(), k[2 * layer + 1][:2].double().cpu().numpy(),
+                       [1, 1, 0])
+            close(p.o, layer, q[:2], [1, 1, 0], outs[layer][:2], "bf16")
+            assert (outs[layer][2:] == 9.0).all()
+        p.same()
+
+
+def test_overlapping_attention_calls_agree_with_single_ones():
+    p = Pair(P=400, H=2, D=128, B=2, W=200)
+    p.reserve([12000, 7000])
+    p.put(torch.randn(19000, 2, 128, device="cuda"), torch.randn(19000, 2, 128, device="cuda"), [12000, 7000])
+    qs = [p.query([1, 1], 8, "f16") for _ in range(8)] + [p.query([40, 33], 8, "f16") for _ in range(2)]
+    cus = [cu_of([1, 1])] * 8 + [cu_of([40, 33])] * 2
+    alone = [p.c.attend(0, q, cu=cu) for q, cu in zip(qs, cus)]
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        got = []
+        for i, (q, cu) in enumerate(zip(qs, cus)):
+            with torch.cuda.stream(streams[i % 3]):
+                got.append(p.c.attend(0, q, cu=cu))
+        torch.cuda.synchronize()
+        for a, b in zip(alone, got):
+            assert torch.equal(a, b)                   # the same bits: no result depends on who runs beside it
+    p.c.check()
+
+
+def test_the_operators_together_over_a_search():
+    """Prompt, then several beams decode, are reordered, trimmed to the window
+    and packed, in every layer."""
+    p = Pair(L=2, P=64, H=2, D=128, B=4, W=10, seed=5)
+    window, sinks = 150, 4
+    p.grow([400], "bf16", seqs=[0])
+    for layer in range(2):
+        p.attend_close([400], 4, "bf16", window, sinks, seqs=[0], layer=layer)
+    p.fork([0, 0, 0], [1, 2, 3])
+    for t in range(6):
+        p.grow([1] * 4, "bf16")
+        for layer in range(2):
+            p.attend_close([1] * 4, 4, "bf16", window, sinks, layer=layer, max_q=1)
+        if t % 2:
+            p.fork(p.rng.integers(0, 4, 4).tolist(), [0, 1, 2, 3])
+        if t == 2:
+            p.release([0, 1, 2, 3], window, sinks)
+        if t == 4:
+            p.compact()
+        p.same()
+    p.release([0, 1, 2, 3])
+    p.same()
+    assert int(p.c.refs.sum()) == 0

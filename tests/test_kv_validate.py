@@ -1,0 +1,161 @@
+"""The key/value cache calls check what the host can see before any CUDA call
+(no GPU: the pointers are placeholders that the checks never follow), and the
+ctypes mirrors of their structs have the header's layout."""
+import ctypes
+import os
+import re
+import shutil
+import subprocess
+
+import pytest
+import torch
+
+from sparse_activation_decode_gb300 import KvCache
+from sparse_activation_decode_gb300 import _lib as L
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+FAKE = 0x100000
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from sparse_activation_decode_gb300.build import build
+    build()
+    return L.load()
+
+
+def desc(**kw):
+    d = L.KvDesc()
+    d.n_layers, d.n_pages, d.n_kv_heads, d.head_dim, d.max_seqs, d.max_pages = 2, 16, 4, 128, 8, 5
+    for f in ("k", "v", "k_scale", "v_scale", "table", "lengths", "refs", "work"):
+        setattr(d, f, FAKE)
+    for k, v in kw.items():
+        setattr(d, k, v)
+    return d
+
+
+def batch(**kw):
+    b = L.KvBatch(None, FAKE, 4, 10, 10)
+    for k, v in kw.items():
+        setattr(b, k, v)
+    return b
+
+
+def attn(lib, d=None, **kw):
+    ws = lib.np_kv_attend_workspace(ctypes.byref(d or desc()))
+    t = L.KvAttn(FAKE, 2 * FAKE, 8 * 128, 128, 8 * 128, 128, 4 * FAKE, ws, 8, L.NP_F16, 0.1, 0, 0)
+    for k, v in kw.items():
+        setattr(t, k, v)
+    return t
+
+
+BAD_DESC = {
+    "no layers": dict(n_layers=0), "no pages": dict(n_pages=0), "no heads": dict(n_kv_heads=0),
+    "257 heads": dict(n_kv_heads=257), "head_dim 96": dict(head_dim=96), "head_dim 0": dict(head_dim=0),
+    "no seqs": dict(max_seqs=0), "no table": dict(max_pages=0), "table too wide": dict(max_pages=1 << 26),
+    "too many blocks": dict(n_layers=1 << 12, n_pages=1 << 20),
+    "k null": dict(k=None), "v unaligned": dict(v=FAKE + 16), "scales null": dict(k_scale=None),
+    "scale unaligned": dict(v_scale=FAKE + 4), "table null": dict(table=None), "lengths null": dict(lengths=None),
+    "refs unaligned": dict(refs=FAKE + 4), "work null": dict(work=None),
+}
+
+
+@pytest.mark.parametrize("name", list(BAD_DESC))
+def test_every_call_refuses_a_bad_description(lib, name):
+    d = ctypes.byref(desc(**BAD_DESC[name]))
+    b, t = ctypes.byref(batch()), ctypes.byref(attn(lib))
+    for st in (lib.np_kv_reserve(d, None, FAKE, 4, None), lib.np_kv_fork(d, FAKE, FAKE, 4, None),
+               lib.np_kv_release(d, FAKE, 4, 0, 0, None), lib.np_kv_compact(d, None), lib.np_kv_check(d, None),
+               lib.np_kv_append(d, 0, b, FAKE, 512, 128, FAKE, 512, 128, L.NP_F16, None),
+               lib.np_kv_attend(d, 0, b, t, None)):
+        assert st == L.NP_ERR_ARG
+        assert b"np_kv_" in lib.np_last_error()
+
+
+@pytest.mark.parametrize("kw", [dict(n_seqs=0), dict(n_seqs=1025), dict(n_tokens=-1), dict(max_tokens=-1),
+                                dict(n_seqs=9), dict(cu=None), dict(cu=None, n_tokens=8, max_tokens=1),
+                                dict(cu=FAKE + 2), dict(seqs=FAKE + 1)], ids=str)
+def test_bad_batches_are_refused(lib, kw):
+    d, b = ctypes.byref(desc()), ctypes.byref(batch(**kw))
+    assert lib.np_kv_append(d, 0, b, FAKE, 512, 128, FAKE, 512, 128, L.NP_F16, None) == L.NP_ERR_ARG
+    assert lib.np_kv_attend(d, 0, b, ctypes.byref(attn(lib)), None) == L.NP_ERR_ARG
+
+
+@pytest.mark.parametrize("kw", [dict(q=None), dict(out=None), dict(q=FAKE + 1), dict(q_token_stride=-1),
+                                dict(out_head_stride=-128), dict(workspace=None), dict(workspace=FAKE + 8),
+                                dict(workspace_bytes=0), dict(n_heads=0), dict(n_heads=6), dict(n_heads=2048),
+                                dict(dtype=3), dict(dtype=-1), dict(scale=0.0), dict(scale=-1.0),
+                                dict(scale=float("nan")), dict(scale=float("inf")), dict(window=-1),
+                                dict(sinks=-1)], ids=str)
+def test_bad_attention_arguments_are_refused(lib, kw):
+    assert lib.np_kv_attend(ctypes.byref(desc()), 0, ctypes.byref(batch()), ctypes.byref(attn(lib, **kw)),
+                            None) == L.NP_ERR_ARG
+
+
+def test_bad_layers_lists_and_tensors_are_refused(lib):
+    d, b, t = ctypes.byref(desc()), ctypes.byref(batch()), ctypes.byref(attn(lib))
+    for layer in (-1, 2):
+        assert lib.np_kv_attend(d, layer, b, t, None) == L.NP_ERR_ARG
+        assert lib.np_kv_append(d, layer, b, FAKE, 512, 128, FAKE, 512, 128, L.NP_F16, None) == L.NP_ERR_ARG
+    assert lib.np_kv_append(d, 0, b, None, 512, 128, FAKE, 512, 128, L.NP_F16, None) == L.NP_ERR_ARG
+    assert lib.np_kv_append(d, 0, b, FAKE, 512, -128, FAKE, 512, 128, L.NP_F16, None) == L.NP_ERR_ARG
+    assert lib.np_kv_append(d, 0, b, FAKE + 2, 512, 128, FAKE, 512, 128, L.NP_F32, None) == L.NP_ERR_ARG
+    assert lib.np_kv_append(d, 0, b, FAKE, 512, 128, FAKE, 512, 128, 7, None) == L.NP_ERR_ARG
+    for n in (0, -1, 1025):
+        assert lib.np_kv_reserve(d, FAKE, FAKE, n, None) == L.NP_ERR_ARG
+        assert lib.np_kv_fork(d, FAKE, FAKE, n, None) == L.NP_ERR_ARG
+        assert lib.np_kv_release(d, FAKE, n, 0, 0, None) == L.NP_ERR_ARG
+    assert lib.np_kv_reserve(d, None, FAKE, 9, None) == L.NP_ERR_ARG
+    assert lib.np_kv_reserve(d, None, None, 4, None) == L.NP_ERR_ARG
+    assert lib.np_kv_fork(d, FAKE, None, 4, None) == L.NP_ERR_ARG
+    assert lib.np_kv_fork(d, FAKE, FAKE, 9, None) == L.NP_ERR_ARG
+    assert lib.np_kv_release(d, FAKE, 4, -1, 0, None) == L.NP_ERR_ARG
+    assert lib.np_kv_release(d, FAKE, 4, 1, -1, None) == L.NP_ERR_ARG
+
+
+def test_no_tokens_is_a_call_that_does_nothing(lib):
+    d, b = ctypes.byref(desc()), ctypes.byref(batch(n_tokens=0))
+    assert lib.np_kv_append(d, 0, b, None, 0, 0, None, 0, 0, L.NP_F16, None) == L.NP_OK
+    assert lib.np_kv_attend(d, 0, b, ctypes.byref(attn(lib, q=None, out=None)), None) == L.NP_OK
+
+
+def test_work_words_cover_every_list(lib):
+    d = desc()
+    words = lib.np_kv_work_words(ctypes.byref(d))
+    assert words >= 4 + 2 * max(d.n_pages // 2 + 1, d.max_seqs) + d.max_seqs + d.n_pages + d.max_seqs * d.max_pages
+    assert lib.np_kv_work_words(ctypes.byref(desc(head_dim=80))) == -1
+    assert lib.np_kv_work_words(None) == -1 and lib.np_kv_attend_workspace(None) == -1
+
+
+def test_cache_refuses_host_tensors_and_bad_sizes():
+    with pytest.raises(ValueError):
+        KvCache(n_layers=1, n_pages=0, n_kv_heads=1, head_dim=64, max_seqs=1, max_pages=1, device="cuda:0")
+    k = torch.zeros(1, 2, 1, 64, 64, dtype=torch.uint8).view(torch.float8_e4m3fn)
+    s = torch.zeros(1, 2, 1)
+    i = torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        KvCache.wrap(k, k, s, s, torch.zeros(2, 2, dtype=torch.int32), i, i)
+
+
+STRUCTS = {"np_kv_desc": "KvDesc", "np_kv_batch": "KvBatch", "np_kv_attn": "KvAttn"}
+
+
+@pytest.mark.parametrize("cname", list(STRUCTS))
+def test_struct_matches_header(tmp_path, cname):
+    cc = shutil.which("gcc") or shutil.which("cc")
+    if cc is None:
+        pytest.skip("no host C compiler")
+    cls = getattr(L, STRUCTS[cname])
+    with open(os.path.join(ROOT, "include", "np.h")) as f:
+        text = re.sub(r"/\*.*?\*/", "", f.read(), flags=re.S)
+    body = re.search(r"typedef struct \{([^{}]*)\}\s*" + cname + ";", text).group(1)
+    assert re.findall(r"(\w+)\s*;", body) == [f for f, _ in cls._fields_]
+    src = tmp_path / "layout.c"
+    src.write_text('#include <stddef.h>\n#include <stdio.h>\n#include "np.h"\nint main(void) {\n'
+                   + f'  printf("%zu\\n", sizeof({cname}));\n'
+                   + "".join(f'  printf("%zu\\n", offsetof({cname}, {f}));\n' for f, _ in cls._fields_)
+                   + "  return 0;\n}\n")
+    exe = tmp_path / "layout"
+    subprocess.run([cc, "-std=c99", "-I", os.path.join(ROOT, "include"), str(src), "-o", str(exe)], check=True)
+    out = [int(x) for x in subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout.split()]
+    assert out == [ctypes.sizeof(cls)] + [getattr(cls, f).offset for f, _ in cls._fields_]
