@@ -240,6 +240,9 @@ struct MmaPlan {
 struct RowMaps {
   CUtensorMap m32, m8;
 };
+// Tensor map of e4m3 pages [blocks][64][dim] with boxes of one page (of 128
+// columns at most); 128-byte swizzle unless the rows are shorter.
+cudaError_t make_page_map(CUtensorMap* out, const void* base, int dim, uint64_t blocks);
 cudaError_t make_row_maps(RowMaps* out, const void* base, int dtype, uint64_t rows, uint64_t cols);
 size_t mma_smem_bytes(int mode, int ks_len, int n_stages);
 // want_clusters > 0 caps the clusters; max_stages > 1 caps the ring depth.

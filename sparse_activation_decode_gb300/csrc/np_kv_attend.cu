@@ -1,88 +1,814 @@
-// Attention over the 8-bit paged key/value cache (np_kv_attend).
+// Attention over the 8-bit paged key/value cache (np_kv_attend), streaming
+// kernel: single tokens, short prompts, and every case the tiled kernel does
+// not take.
 //
-// One warp per (new token, query head): lane l holds D/32 neighbouring
-// elements of q and of the output, and the warp walks the visible keys one
-// after another with a running maximum and sum, all in fp32:
-//   s_j = (q . k_j) * k_scale * scale,  m' = max(m, s_j),
-//   l' = l 2^(m - m') + 2^(s_j - m'),  o' = o 2^(m - m') + 2^(s_j - m') v_j.
+// Per key/value head the rows of a tile (R = 8 or 16: new tokens x the query
+// heads that share the head) see a list of 64-token pages:
+//   S = (q . K) k_scale scale,  O += softmax weights . V v_scale,
+// with a running maximum m and sum l per row (2^x throughout).
+//
+// Matrix products run transposed on mma.sync m16n8k16, S^T = K Q^T and
+// O^T = V^T P^T: the page is the 16-row operand and the few rows are the 8
+// columns, so a single token wastes 7 of 8 columns instead of 15 of 16 rows,
+// and both e4m3 operands are read as they lie (K by token, V by element).
+// e4m3 is exact in fp16, so no value of the cache is rounded.  q goes in as
+// fp16 after an exact scaling of each row by a power of two (bf16 and fp16
+// queries keep every bit down to 2^-28 of the row's largest), fp32 queries as
+// the sum of two fp16 parts (22 bits).  The weights go in as fp16 scaled by
+// 2^15 (11 bits, 22 for fp32 outputs), which keeps weights down to 2^-29 of
+// the largest normal; sums, maxima and the accumulator are fp32.  The scale
+// of a page's values multiplies that page's fp32 partial sum.
+//
+// Layout of the work: contraction indices are permuted so that each thread
+// reads 16 contiguous bytes: lane 4r + j takes elements [32 j, 32 j + 32) of
+// token 16 (r / 2) + 2 u + r % 2 (u = 0..7), and the same tokens 16 j + ..
+// of V's rows, which makes the 8x8 transposition of the weights (movmatrix)
+// the only exchange between the products.
+//
+// The pages of all sequences and heads form one list, cut into equal
+// contiguous shares, one CTA per SM (ragged lengths balance by construction).
+// In a CTA a producer warp streams pages through a shared-memory ring (TMA,
+// 128-byte swizzle for K so that the 16-byte reads meet no bank twice) and
+// eight warps each take every eighth page, with statistics of their own that
+// are joined once per share.  A row whose pages are cut between CTAs leaves
+// fp32 partials, which a second launch joins in a fixed order.  Short items
+// are not cut (see plan()).
+//
+// Bound: HBM, 2 D bytes per visible token and head.
+//
+// Every wait is bounded (about one second): a timeout is recorded in the
+// cache's error word, the rest of the work is skipped and the copies in
+// flight are drained before the CTA ends.
+#include <cstring>
+
 #include "np_kv.cuh"
+#include "np_tc.cuh"
 
 namespace np {
 
 namespace {
 
-template <typename T, int D>
-__global__ void __launch_bounds__(128) attend_simple_kernel(const KvAttend a) {
-  constexpr int E = D / 32;
-  const int warp = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const int tok = warp / a.Hq, h = warp % a.Hq;
-  if (tok >= a.batch.n_tokens) return;
-  KvSeq s{};
-  bool found = false;
-  for (int i = 0; i < a.batch.n_seqs; ++i) {
-    const KvSeq t = kv_seq(a.kv, a.batch, i);
-    if (tok >= t.begin && tok < t.begin + t.n) {
-      s = t;
-      found = true;
+constexpr int kMaxCtas = 256;       // upper bound of the grid (workspace)
+constexpr int kMaxAttendStages = 16;
+constexpr int kWholePages = 8;      // items of at most this many pages are never cut
+
+template <int D> struct Shape {
+  static constexpr int kWarps = D == 256 ? 4 : 8;           // consumer warps
+  static constexpr int kThreads = 32 * (kWarps + 1);
+  static constexpr int kStage = 2 * kKvPage * D;            // bytes of one page, K then V
+  static constexpr int kRowPad = D + 4;                     // floats per row of the join buffer
+};
+
+// What a CTA knows of the call: its own copy of the sequences' numbers.
+struct Plan {
+  long long chunk;   // units per CTA
+  long long total;   // units
+  int split;         // 1: unit = page, items may be cut; 0: unit = item
+};
+
+struct SeqWork {
+  int row, begin, n, len;
+};
+
+// Pages that a sequence's new tokens see: slots [0, sink) and [lo, hi).
+struct Pages {
+  int sink, lo, count;
+  __device__ __forceinline__ int slot(int k) const { return k < sink ? k : lo + (k - sink); }
+};
+
+__device__ __forceinline__ Pages pages_of(const KvAttend& a, int len, int n) {
+  const int hi = (len + kKvPage - 1) / kKvPage;
+  Pages p;
+  p.lo = p.sink = 0;
+  if (a.window > 0) {
+    const long long first = (long long)len - n - a.window + 1;
+    p.lo = first > 0 ? (int)(first / kKvPage) : 0;
+    const int s = a.sinks / kKvPage + (a.sinks % kKvPage != 0);
+    p.sink = s < p.lo ? s : p.lo;
+  }
+  p.count = p.sink + hi - p.lo;
+  if (p.count < 1) p.count = 1;  // an item without keys still writes its zeros
+  return p;
+}
+
+// Number the units: pre[i] = units before sequence i.  Called by the whole
+// CTA; sequence numbers land in seq[].  Items are (sequence, head, tile).
+// Cutting pays when the longest run of whole items on one CTA is longer than
+// an equal share plus the second launch (about as long as 8 pages:
+// one CTA streams a page of 128-element heads in 0.37 us).
+template <int R>
+__device__ __forceinline__ Plan plan(const KvAttend& a, int ctas, long long* pre, SeqWork* seq, long long* tmp) {
+  const int n = a.batch.n_seqs, g = a.Hq / a.kv.H;
+  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+    const KvSeq s = kv_seq(a.kv, a.batch, i);
+    seq[i] = SeqWork{s.row, s.begin, s.n, s.len};
+  }
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    long long items = 0, pages = 0;
+    int longest = 0;
+    for (int i = lane; i < n; i += 32) {
+      const long long t = (long long)((seq[i].n * (long long)g + R - 1) / R) * a.kv.H;
+      const int c = pages_of(a, seq[i].len, seq[i].n).count;
+      items += t;
+      pages += t * c;
+      if (t && c > longest) longest = c;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      items += __shfl_xor_sync(0xffffffffu, items, o);
+      pages += __shfl_xor_sync(0xffffffffu, pages, o);
+      const int l = __shfl_xor_sync(0xffffffffu, longest, o);
+      longest = l > longest ? l : longest;
+    }
+    const long long per = (items + ctas - 1) / ctas;
+    const bool split = longest > kWholePages && per * longest > pages / ctas + kWholePages;
+    const long long total = split ? pages : items;
+    long long run = 0;
+    for (int base = 0; base < n; base += 32) {
+      const int i = base + lane;
+      long long u = 0;
+      if (i < n) {
+        u = (long long)((seq[i].n * (long long)g + R - 1) / R) * a.kv.H;
+        if (split) u *= pages_of(a, seq[i].len, seq[i].n).count;
+      }
+      long long x = u;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (i < n) pre[i] = run + x - u;
+      run += __shfl_sync(0xffffffffu, x, 31);
+    }
+    if (lane == 0) {
+      pre[n] = total;
+      tmp[0] = (total + ctas - 1) / ctas;
+      tmp[1] = split;
     }
   }
-  if (!found) return;
-  const int pos = s.len - s.n + tok - s.begin;
-  const int kvh = h / (a.Hq / a.kv.H);
-  const T* q = static_cast<const T*>(a.q) + tok * a.q_tok + h * a.q_head + lane * E;
-  float qv[E], o[E], m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int i = 0; i < E; ++i) {
-    qv[i] = kv_to_float<T>(q[i]);
-    o[i] = 0.f;
+  __syncthreads();
+  Plan p;
+  p.chunk = tmp[0] > 0 ? tmp[0] : 1;
+  p.total = pre[n];
+  p.split = (int)tmp[1];
+  return p;
+}
+
+// The sequence that holds unit u.
+__device__ __forceinline__ int seq_of(const long long* pre, int n, long long u) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (pre[mid] <= u) lo = mid; else hi = mid;
   }
-  for (int j = 0; j <= pos; ++j) {
-    if (a.window > 0 && j <= pos - a.window && j >= a.sinks) {
-      j = pos - a.window;
-      continue;
-    }
-    const int page = a.kv.table[(size_t)s.row * a.kv.max_pages + j / kKvPage];
-    if (page < 0 || page >= a.kv.n_pages) {
-      if (page != -1) atomicExch(a.kv.err, kDevErrBounds);
-      continue;
-    }
-    const size_t block = (size_t)page * a.kv.H + kvh;
-    const uint8_t* k = a.kv.k + (block * kKvPage + j % kKvPage) * D + lane * E;
-    float x = 0.f;
-#pragma unroll
-    for (int i = 0; i < E; ++i) x = fmaf(qv[i], f16x2_to_f32x2(e4m3x2_to_f16x2(k[i])).x, x);
-    x = warp_sum(x) * a.kv.k_scale[block] * a.scale_log2;
-    const float mn = fmaxf(m, x), ref = mn == -INFINITY ? 0.f : mn;
-    const float c = exp2f(m - ref), p = exp2f(x - ref);
-    const float pv = p * a.kv.v_scale[block];
-    const uint8_t* v = a.kv.v + (block * D + lane * E) * kKvPage + j % kKvPage;
-    l = l * c + p;
-#pragma unroll
-    for (int i = 0; i < E; ++i) o[i] = fmaf(pv, f16x2_to_f32x2(e4m3x2_to_f16x2(v[i * kKvPage])).x, o[i] * c);
-    m = mn;
+  return lo;
+}
+
+// A stretch of pages [k0, k1) of one item.
+struct Segment {
+  int b, h, tile, k0, k1;
+  Pages pages;
+  bool starts, ends;  // the stretch holds the item's first / last page
+};
+
+template <int R>
+__device__ __forceinline__ Segment segment_at(const KvAttend& a, const Plan& p, const long long* pre,
+                                              const SeqWork* seq, long long u, long long end) {
+  Segment s;
+  s.b = seq_of(pre, a.batch.n_seqs, u);
+  const SeqWork w = seq[s.b];
+  s.pages = pages_of(a, w.len, w.n);
+  const int g = a.Hq / a.kv.H;
+  const int tiles = (int)((w.n * (long long)g + R - 1) / R);
+  const long long off = u - pre[s.b];
+  const long long item = p.split ? off / s.pages.count : off;
+  s.h = (int)(item / tiles);
+  s.tile = (int)(item % tiles);
+  if (p.split) {
+    s.k0 = (int)(off - item * s.pages.count);
+    const long long left = end - u;
+    s.k1 = (long long)(s.pages.count - s.k0) < left ? s.pages.count : s.k0 + (int)left;
+  } else {
+    s.k0 = 0;
+    s.k1 = s.pages.count;
   }
-  T* out = static_cast<T*>(a.out) + tok * a.o_tok + h * a.o_head + lane * E;
-  const float inv = l == 0.f ? 0.f : 1.f / l;
+  s.starts = s.k0 == 0;
+  s.ends = s.k1 == s.pages.count;
+  return s;
+}
+
+// Rows of a tile and the positions they span.
+struct TileRows {
+  int rows, p_min, p_max;
+};
+template <int R>
+__device__ __forceinline__ TileRows tile_rows(const KvAttend& a, const SeqWork& w, int tile) {
+  const int g = a.Hq / a.kv.H;
+  const long long all = w.n * (long long)g;
+  TileRows t;
+  t.rows = (int)(all - (long long)tile * R < R ? all - (long long)tile * R : R);
+  t.p_min = w.len - w.n + tile * R / g;
+  if (t.p_min < -1) t.p_min = -1;  // before the first key: nothing to see either way
+  t.p_max = w.len - w.n + (tile * R + t.rows - 1) / g;
+  if (t.p_max < -1) t.p_max = -1;
+  return t;
+}
+
+__device__ __forceinline__ bool page_seen(const KvAttend& a, const TileRows& t, int base) {
+  return base <= t.p_max && (a.window == 0 || base + kKvPage - 1 > t.p_min - a.window || base < a.sinks);
+}
+// Every row of the tile sees every token of the page.
+__device__ __forceinline__ bool page_whole(const KvAttend& a, const TileRows& t, int base) {
+  return base + kKvPage - 1 <= t.p_min &&
+         (a.window == 0 || base > t.p_max - a.window || base + kKvPage - 1 < a.sinks);
+}
+
+__device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar,
+                                            uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar), "l"(policy)
+      : "memory");
+}
+
+// A number that is not NaN in both halves: what a masked place holds never
+// reaches a sum as NaN (its weight is zero).
+__device__ __forceinline__ uint32_t no_nan(uint32_t v) {
+  const __half2 h = __hmin2(*reinterpret_cast<__half2*>(&v), __floats2half2_rn(448.f, 448.f));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+struct StageMeta {
+  uint32_t seq;  // number of the page in this CTA, plus 1
+  int base;      // position of the page's first token; -1: nothing in this stage
+  float k_scale, v_scale;
+};
+
+// Wait for a phase unless the CTA has given up already.
+__device__ __forceinline__ bool wait_stage(uint64_t* bar, uint32_t parity, volatile int* abort, int* err) {
+  return wait_phase(smem_addr(bar), parity, abort, err);
+}
+
+// Wait for page i in stage st.  Pages land in any order and a stage's pages
+// belong to different warps, so a warp may come before the stage's previous
+// page has landed; the barrier's parity cannot tell that from its own page
+// being there.  The page's number can: the producer writes it when it has the
+// stage to itself again, after which the parity is unambiguous.
+__device__ __forceinline__ bool wait_page(volatile StageMeta* meta, uint64_t* bar, uint32_t i, uint32_t parity,
+                                          volatile int* abort, int* err) {
+  if (meta->seq != i + 1) {
+    const uint64_t t0 = global_ns();
+    for (uint32_t it = 1; meta->seq != i + 1; ++it) {
+      if ((it & 127u) == 0) {
+        if (*abort) return false;
+        if (global_ns() - t0 > kWaitLimitNs) {
+          atomicExch(err, kDevErrTimeout);
+          *abort = 1;
+          return false;
+        }
+      }
+    }
+  }
+  return wait_stage(bar, parity, abort, err);
+}
+
+// Partials of cut items: slot 2c for a stretch of CTA c that continues an
+// item, 2c + 1 for one that begins an item it does not end.
+template <int D, int R> struct Partial {
+  static constexpr size_t kFloats = (size_t)R * (D + 2);
+  __device__ static float* o(void* ws, int slot) { return static_cast<float*>(ws) + slot * kFloats; }
+  __device__ static float* m(void* ws, int slot) { return o(ws, slot) + R * D; }
+  __device__ static float* l(void* ws, int slot) { return o(ws, slot) + R * D + R; }
+};
+
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(Shape<D>::kThreads, 1)
+    attend_stream_kernel(const __grid_constant__ CUtensorMap kmap, const KvAttend a, int n_stages) {
+  using Sh = Shape<D>;
+  constexpr int R = 8 * NT;
+  constexpr int W = Sh::kWarps;
+  constexpr int NP = sizeof(T) == 4 ? 2 : 1;          // fp16 parts of q and of the weights
+  constexpr int KH = D == 256 ? 2 : 1;                // 128-byte column blocks of a K page
+  constexpr int KC = (D >= 128 ? 2 : 1);              // 16-byte chunks a thread reads of a token's block
+  constexpr int KS = D / 16;                          // contraction steps of S
+  constexpr int MD = D / 16;                          // 16-element tiles of the output
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t full[kMaxAttendStages], empty[kMaxAttendStages];
+  __shared__ StageMeta meta[kMaxAttendStages];
+  __shared__ long long tmp[2];
+  __shared__ int abort_s;
+  __shared__ float stat_m[W][R], stat_l[W][R];
+
+  // ring (1024-byte aligned), join buffer, sequence numbers
+  uint8_t* ring = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
+  float* join = reinterpret_cast<float*>(ring + (size_t)n_stages * Sh::kStage);
+  long long* pre = reinterpret_cast<long long*>(join + W * R * Sh::kRowPad);
+  SeqWork* seq = reinterpret_cast<SeqWork*>(pre + a.batch.n_seqs + 1 + ((a.batch.n_seqs + 1) & 1));
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < n_stages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+      meta[i].seq = 0;
+    }
+    abort_s = 0;
+    fence_barrier_init();
+  }
+  const Plan p = plan<R>(a, gridDim.x, pre, seq, tmp);
+  grid_dependents_launch();
+  const long long u0 = (long long)blockIdx.x * p.chunk;
+  const long long u1 = u0 + p.chunk < p.total ? u0 + p.chunk : p.total;
+  const int g = a.Hq / a.kv.H;
+  const uint32_t ns = (uint32_t)n_stages;
+
+  if (warp == W) {
+    // ---- producer ----
+    const uint64_t once = policy_evict_first();
+    uint32_t count = 0;  // pages handed out
+    bool alive = true;
+    for (long long u = u0; u < u1 && alive;) {
+      const Segment s = segment_at<R>(a, p, pre, seq, u, u1);
+      const SeqWork w = seq[s.b];
+      const TileRows t = tile_rows<R>(a, w, s.tile);
+      for (int k0 = s.k0; k0 < s.k1 && alive; k0 += 32) {
+        // 32 pages at a time: table entries and scales come in parallel
+        const int k = k0 + lane;
+        int page = -1, base = 0;
+        float ks = 0.f, vs = 0.f;
+        if (k < s.k1) {
+          const int slot = s.pages.slot(k);
+          base = slot * kKvPage;
+          if (base < w.len && page_seen(a, t, base)) {
+            page = a.kv.table[(size_t)w.row * a.kv.max_pages + slot];
+            if (page < 0 || page >= a.kv.n_pages) {
+              if (page != -1) atomicExch(a.kv.err, kDevErrBounds);
+              page = -1;
+            } else {
+              ks = a.kv.k_scale[(size_t)page * a.kv.H + s.h];
+              vs = a.kv.v_scale[(size_t)page * a.kv.H + s.h];
+            }
+          }
+        }
+        const int here = s.k1 - k0 < 32 ? s.k1 - k0 : 32;
+        for (int i = 0; i < here; ++i) {
+          const int pg = __shfl_sync(0xffffffffu, page, i), bs = __shfl_sync(0xffffffffu, base, i);
+          const float ksi = __shfl_sync(0xffffffffu, ks, i), vsi = __shfl_sync(0xffffffffu, vs, i);
+          const uint32_t st = count % ns;
+          if (count >= ns) alive = wait_stage(&empty[st], (count / ns - 1) & 1, &abort_s, a.kv.err);
+          alive = __shfl_sync(0xffffffffu, (int)alive, 0) != 0;
+          if (!alive) break;
+          if (lane == 0) {
+            meta[st].base = pg < 0 ? -1 : bs;
+            meta[st].k_scale = ksi;
+            meta[st].v_scale = vsi;
+            *reinterpret_cast<volatile uint32_t*>(&meta[st].seq) = count + 1;
+            if (pg < 0) {
+              mbar_arrive_local(smem_addr(&full[st]));
+            } else {
+              const int block = pg * a.kv.H + s.h;
+              uint8_t* dst = ring + (size_t)st * Sh::kStage;
+              mbar_arrive_expect_tx(&full[st], Sh::kStage);
 #pragma unroll
-  for (int i = 0; i < E; ++i) out[i] = kv_from_float<T>(o[i] * inv);
+              for (int x = 0; x < KH; ++x)
+                tma_load_3d(smem_addr(dst) + x * 8192, &kmap, x * 128, 0, block, smem_addr(&full[st]), once);
+              bulk_load(dst + kKvPage * D, a.kv.v + (size_t)block * kKvPage * D, kKvPage * D, &full[st], once);
+            }
+          }
+          __syncwarp();
+          ++count;
+        }
+      }
+      u = p.split ? u + (s.k1 - s.k0) : u + 1;
+    }
+    if (abort_s) {
+      // drain: no copy may land after the CTA has gone
+      for (uint32_t c = count > ns ? count - ns : 0; c < count; ++c) {
+        const uint64_t t0 = global_ns();
+        while (!mbar_try_wait(&full[c % ns], (c / ns) & 1))
+          if (global_ns() - t0 > kWaitLimitNs) break;
+      }
+    }
+    return;
+  }
+
+  // ---- consumers ----
+  const int r = lane >> 2, j = lane & 3;
+  uint32_t count = 0;
+  bool alive = true;
+  for (long long u = u0; u < u1;) {
+    const Segment s = segment_at<R>(a, p, pre, seq, u, u1);
+    const SeqWork w = seq[s.b];
+    const TileRows t = tile_rows<R>(a, w, s.tile);
+    const int n_pages = s.k1 - s.k0;
+
+    // q: lane 4r + j holds elements [32 j, 32 j + 32) (+128 x) of row r of
+    // each group of 8 rows, as fp16 parts, and the factor of each of its two
+    // columns' logits (rows 2 j and 2 j + 1)
+    uint32_t qf[NT][NP][KS][2];
+    float fac[NT][2];
+    int pos[NT][2];
+    if (warp < n_pages) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const int row = nt * 8 + r;
+        const bool in = row < t.rows;
+        const int at = s.tile * R + row;
+        const T* q = static_cast<const T*>(a.q) + (long long)(w.begin + at / g) * a.q_tok +
+                     (long long)(s.h * g + at % g) * a.q_head;
+        float x[KS * 4];
+        float top = 0.f;
+#pragma unroll
+        for (int c = 0; c < KS / 4; ++c) {
+          // chunk c of a thread: 16 elements
+          const int d = D == 64 ? 16 * j : 128 * (c / 2) + 32 * j + 16 * (c % 2);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) x[16 * c + e] = in ? kv_to_float<T>(q[d + e]) : 0.f;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) top = fmaxf(top, fabsf(x[16 * c + e]));
+        }
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // largest element to [2^14, 2^15): exact, and far from fp16's ends
+        int e = (int)(__float_as_uint(top) >> 23) - 127;
+        e = e < -112 ? -112 : e;
+        const float up = __uint_as_float((uint32_t)(14 - e + 127) << 23);
+        const float down = __uint_as_float((uint32_t)(e - 14 + 127) << 23) * a.scale_log2;
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float lo = x[4 * k + 2 * h] * up, hi = x[4 * k + 2 * h + 1] * up;
+            qf[nt][0][k][h] = pack_f16(lo, hi);
+            if constexpr (NP == 2) {
+              const float2 f = f16x2_to_f32x2(qf[nt][0][k][h]);
+              qf[nt][NP - 1][k][h] = pack_f16(lo - f.x, hi - f.y);
+            }
+          }
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          // row 2 j + c lives in lanes 4 (2 j + c) ..
+          fac[nt][c] = __shfl_sync(0xffffffffu, down, 4 * (2 * j + c));
+          const int rc = nt * 8 + 2 * j + c;
+          const int ps = w.len - w.n + (s.tile * R + rc) / g;
+          pos[nt][c] = rc < t.rows && ps > -1 ? ps : -1;
+        }
+      }
+    }
+
+    float o[NT][MD][4], m[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        m[nt][c] = -INFINITY;
+        l[nt][c] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < MD; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[nt][i][c] = 0.f;
+    }
+
+    for (int k = warp; k < n_pages && alive; k += W) {
+      const uint32_t i = count + k, st = i % ns;
+      alive = wait_page(&meta[st], &full[st], i, (i / ns) & 1, &abort_s, a.kv.err);
+      alive = __all_sync(0xffffffffu, alive);
+      if (!alive) break;
+      const StageMeta mt = meta[st];
+      if (mt.base >= 0) {
+        const uint32_t kp = smem_addr(ring) + st * Sh::kStage, vp = kp + kKvPage * D;
+        const bool whole = page_whole(a, t, mt.base);
+        // S^T, tokens 16 (r / 2) + 2 u + r % 2 in rows, u = 2 mt and 2 mt + 1
+        float sacc[NT][4][4];
+#pragma unroll
+        for (int mi = 0; mi < 4; ++mi) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) sacc[nt][mi][c] = 0.f;
+          const int t0 = 16 * (r >> 1) + 4 * mi + (r & 1), t1 = t0 + 2;
+#pragma unroll
+          for (int x = 0; x < KH; ++x)
+#pragma unroll
+            for (int c = 0; c < KC; ++c) {
+              uint4 v0, v1;
+              if constexpr (D == 64) {
+                v0 = lds128(kp + t0 * 64 + 16 * j);
+                v1 = lds128(kp + t1 * 64 + 16 * j);
+              } else {
+                v0 = lds128(kp + x * 8192 + t0 * 128 + (((2 * j + c) ^ (t0 & 7)) << 4));
+                v1 = lds128(kp + x * 8192 + t1 * 128 + (((2 * j + c) ^ (t1 & 7)) << 4));
+              }
+              const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const uint32_t af[4] = {e4m3x2_to_f16x2(w0[q] & 0xffffu), e4m3x2_to_f16x2(w1[q] & 0xffffu),
+                                        e4m3x2_to_f16x2(w0[q] >> 16), e4m3x2_to_f16x2(w1[q] >> 16)};
+                const int ks = (x * KC + c) * 4 + q;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                  for (int pt = 0; pt < NP; ++pt) mma_f16(sacc[nt][mi], af, qf[nt][pt][ks][0], qf[nt][pt][ks][1]);
+              }
+            }
+        }
+        // weights
+        uint32_t pf[NT][NP][8];
+        float alpha[NT][2];
+        bool moved = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float top[2] = {-INFINITY, -INFINITY};
+          const float f[2] = {fac[nt][0] * mt.k_scale, fac[nt][1] * mt.k_scale};
+#pragma unroll
+          for (int mi = 0; mi < 4; ++mi)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              float& x = sacc[nt][mi][c];
+              x *= f[c & 1];
+              if (!whole) {
+                const int tok = mt.base + 16 * (r >> 1) + 4 * mi + 2 * (c >> 1) + (r & 1);
+                const int ps = pos[nt][c & 1];
+                const bool see = tok <= ps && (a.window == 0 || tok > ps - a.window || tok < a.sinks);
+                x = see ? x : -INFINITY;
+              }
+              top[c & 1] = fmaxf(top[c & 1], x);
+            }
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+#pragma unroll
+            for (int sh = 4; sh < 32; sh <<= 1) top[c] = fmaxf(top[c], __shfl_xor_sync(0xffffffffu, top[c], sh));
+            const float mn = fmaxf(m[nt][c], top[c]);
+            const float ref = mn == -INFINITY ? 0.f : mn;
+            alpha[nt][c] = ex2(m[nt][c] - ref);
+            moved |= mn != m[nt][c];
+            m[nt][c] = mn;
+            top[c] = ref - 15.f;
+          }
+          float sum[2] = {0.f, 0.f};
+#pragma unroll
+          for (int mi = 0; mi < 4; ++mi) {
+            float e[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              e[c] = ex2(sacc[nt][mi][c] - top[c & 1]);
+              sum[c & 1] += e[c];
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t hi = pack_f16(e[2 * h], e[2 * h + 1]);
+              pf[nt][0][2 * mi + h] = transpose8x8(hi);
+              if constexpr (NP == 2) {
+                const float2 b = f16x2_to_f32x2(hi);
+                pf[nt][NP - 1][2 * mi + h] = transpose8x8(pack_f16(e[2 * h] - b.x, e[2 * h + 1] - b.y));
+              }
+            }
+          }
+#pragma unroll
+          for (int c = 0; c < 2; ++c) l[nt][c] = fmaf(l[nt][c], alpha[nt][c], sum[c]);
+        }
+        if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i2 = 0; i2 < MD; ++i2)
+#pragma unroll
+              for (int c = 0; c < 4; ++c) o[nt][i2][c] *= alpha[nt][c & 1];
+        }
+        // O^T += V^T P^T
+#pragma unroll
+        for (int md = 0; md < MD; ++md) {
+          const uint4 v0 = lds128(vp + (16 * md + r) * 64 + 16 * j), v1 = lds128(vp + (16 * md + r + 8) * 64 + 16 * j);
+          const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
+          float acc[NT][4];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) acc[nt][c] = 0.f;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t af[4] = {e4m3x2_to_f16x2(w0[q] & 0xffffu), e4m3x2_to_f16x2(w1[q] & 0xffffu),
+                              e4m3x2_to_f16x2(w0[q] >> 16), e4m3x2_to_f16x2(w1[q] >> 16)};
+            if (!whole) {
+#pragma unroll
+              for (int c = 0; c < 4; ++c) af[c] = no_nan(af[c]);
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int pt = 0; pt < NP; ++pt) mma_f16(acc[nt], af, pf[nt][pt][2 * q], pf[nt][pt][2 * q + 1]);
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) o[nt][md][c] = fmaf(acc[nt][c], mt.v_scale, o[nt][md][c]);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive_local(smem_addr(&empty[st]));
+    }
+    count += n_pages;
+
+    // join the warps' statistics and accumulators
+    const int parts = n_pages < W ? n_pages : W;
+    if (warp < parts) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float x = l[nt][c];
+#pragma unroll
+          for (int sh = 4; sh < 32; sh <<= 1) x += __shfl_xor_sync(0xffffffffu, x, sh);
+          const int row = nt * 8 + 2 * j + c;
+          if (r == 0) {
+            stat_m[warp][row] = m[nt][c];
+            stat_l[warp][row] = x;
+          }
+          float* dst = join + (warp * R + row) * Sh::kRowPad + r;
+#pragma unroll
+          for (int md = 0; md < MD; ++md) {
+            dst[16 * md] = o[nt][md][c];
+            dst[16 * md + 8] = o[nt][md][c + 2];
+          }
+        }
+    }
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * W) : "memory");
+    const bool cut = !(s.starts && s.ends);
+    const int slot = 2 * blockIdx.x + (s.starts ? 1 : 0);
+    for (int x = tid; x < t.rows * (D / 4); x += 32 * W) {
+      const int row = x / (D / 4), d = x % (D / 4) * 4;
+      float top = -INFINITY, sum = 0.f;
+      for (int i = 0; i < parts; ++i) top = fmaxf(top, stat_m[i][row]);
+      const float ref = top == -INFINITY ? 0.f : top;
+      float y[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int i = 0; i < parts; ++i) {
+        const float f = ex2(stat_m[i][row] - ref);
+        sum = fmaf(stat_l[i][row], f, sum);
+        const float4 v = *reinterpret_cast<const float4*>(join + (i * R + row) * Sh::kRowPad + d);
+        y[0] = fmaf(v.x, f, y[0]);
+        y[1] = fmaf(v.y, f, y[1]);
+        y[2] = fmaf(v.z, f, y[2]);
+        y[3] = fmaf(v.w, f, y[3]);
+      }
+      if (cut) {
+        float* po = Partial<D, R>::o(a.ws, slot) + row * D + d;
+        *reinterpret_cast<float4*>(po) = make_float4(y[0], y[1], y[2], y[3]);
+        if (d == 0) {
+          Partial<D, R>::m(a.ws, slot)[row] = top;
+          Partial<D, R>::l(a.ws, slot)[row] = sum;
+        }
+      } else {
+        const int at = s.tile * R + row;
+        T* out = static_cast<T*>(a.out) + (long long)(w.begin + at / g) * a.o_tok +
+                 (long long)(s.h * g + at % g) * a.o_head + d;
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) out[c] = kv_from_float<T>(y[c] * inv);
+      }
+    }
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * W) : "memory");
+    u = p.split ? u + n_pages : u + 1;
+  }
+}
+
+// Joins the partials of items that were cut.  CTA c looks at the cut between
+// the shares c - 1 and c; the first cut inside an item does the item.
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(256) attend_join_kernel(const KvAttend a, int ctas) {
+  constexpr int R = 8 * NT;
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  __shared__ long long tmp[2];
+  long long* pre = reinterpret_cast<long long*>(smem_raw);
+  SeqWork* seq = reinterpret_cast<SeqWork*>(pre + a.batch.n_seqs + 1 + ((a.batch.n_seqs + 1) & 1));
+  const Plan p = plan<R>(a, ctas, pre, seq, tmp);
+  grid_dependency_wait();
+  const long long u = (long long)blockIdx.x * p.chunk;
+  if (!p.split || u >= p.total) return;
+  const Segment s = segment_at<R>(a, p, pre, seq, u, p.total);
+  if (s.starts) return;                   // the cut falls between two items
+  if (s.k0 > p.chunk) return;             // the previous cut lies inside the same item
+  const SeqWork w = seq[s.b];
+  const TileRows t = tile_rows<R>(a, w, s.tile);
+  const int g = a.Hq / a.kv.H;
+  const int more = (int)((s.pages.count - s.k0 + p.chunk - 1) / p.chunk);  // partials after the first
+  const int c0 = blockIdx.x - 1;
+  for (int x = threadIdx.x; x < t.rows * 32; x += 256) {
+    const int row = x / 32, d = blockIdx.y * 32 + x % 32;
+    float top = Partial<D, R>::m(a.ws, 2 * c0 + 1)[row];
+#pragma unroll 4
+    for (int i = 1; i <= more; ++i) top = fmaxf(top, Partial<D, R>::m(a.ws, 2 * (c0 + i))[row]);
+    const float ref = top == -INFINITY ? 0.f : top;
+    float sum = 0.f, y = 0.f;
+#pragma unroll 4
+    for (int i = 0; i <= more; ++i) {
+      const int slot = 2 * (c0 + i) + (i == 0 ? 1 : 0);
+      const float f = ex2(Partial<D, R>::m(a.ws, slot)[row] - ref);
+      sum = fmaf(Partial<D, R>::l(a.ws, slot)[row], f, sum);
+      y = fmaf(Partial<D, R>::o(a.ws, slot)[row * D + d], f, y);
+    }
+    const int at = s.tile * R + row;
+    T* out = static_cast<T*>(a.out) + (long long)(w.begin + at / g) * a.o_tok +
+             (long long)(s.h * g + at % g) * a.o_head + d;
+    *out = kv_from_float<T>(sum == 0.f ? 0.f : y / sum);
+  }
+}
+
+int sm_count() {
+  static int n[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  if (n[dev] == 0) cudaDeviceGetAttribute(&n[dev], cudaDevAttrMultiProcessorCount, dev);
+  return n[dev];
+}
+
+template <typename T, int D, int NT> struct StreamTag {};
+
+template <typename T, int D, int NT>
+cudaError_t launch_stream(const KvAttend& a, cudaStream_t st) {
+  using Sh = Shape<D>;
+  constexpr int R = 8 * NT;
+  int ctas = sm_count();
+  if (ctas < 1) return cudaErrorInvalidDevice;
+  if (ctas > kMaxCtas) ctas = kMaxCtas;
+  CUtensorMap map;
+  const cudaError_t me = make_page_map(&map, a.kv.k, D, (uint64_t)a.kv.n_pages * a.kv.H);
+  if (me != cudaSuccess) return me;
+  const size_t list = ((size_t)a.batch.n_seqs + 2) * 8 + (size_t)a.batch.n_seqs * sizeof(SeqWork);
+  const size_t fixed = 1024 + (size_t)Sh::kWarps * R * Sh::kRowPad * 4 + list;
+  const size_t room = 225 * 1024;  // of 227 KB; the rest is static
+  int stages = (int)((room - fixed) / Sh::kStage);
+  if (stages > kMaxAttendStages) stages = kMaxAttendStages;
+  const size_t smem = fixed + (size_t)stages * Sh::kStage;
+  auto kern = attend_stream_kernel<T, D, NT>;
+  cudaError_t e = ensure_dyn_smem<StreamTag<T, D, NT>>(reinterpret_cast<const void*>(kern), smem);
+  if (e != cudaSuccess) return e;
+  kern<<<ctas, Sh::kThreads, smem, st>>>(map, a, stages);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  // items too short to be cut leave no partials: a short table row, or a
+  // window (pages of the window, the new tokens and the sinks, and one more
+  // for each end inside a page)
+  long long most = a.kv.max_pages;
+  if (a.window > 0) {
+    const long long seen = ((long long)a.window + a.batch.max_tokens) / kKvPage + a.sinks / kKvPage + 4;
+    if (seen < most) most = seen;
+  }
+  if (most <= kWholePages) return cudaSuccess;
+  PdlConfig pdl(dim3((unsigned)ctas, D / 32), dim3(256), list, st);
+  return cudaLaunchKernelEx(&pdl.cfg, attend_join_kernel<T, D, NT>, a, ctas);
 }
 
 template <typename T>
 cudaError_t launch_typed(const KvAttend& a, cudaStream_t st) {
-  const long long warps = (long long)a.batch.n_tokens * a.Hq;
-  const unsigned grid = (unsigned)((warps + 3) / 4);
-  switch (a.kv.D) {
-    case 64: attend_simple_kernel<T, 64><<<grid, 128, 0, st>>>(a); break;
-    case 128: attend_simple_kernel<T, 128><<<grid, 128, 0, st>>>(a); break;
-    case 256: attend_simple_kernel<T, 256><<<grid, 128, 0, st>>>(a); break;
-    default: return cudaErrorInvalidValue;
-  }
-  return cudaGetLastError();
+  // 16 rows to a tile where there are more than 8 and the registers hold them
+  const bool wide = (long long)a.batch.max_tokens * (a.Hq / a.kv.H) > 8;
+  if (a.kv.D == 64) return wide ? launch_stream<T, 64, 2>(a, st) : launch_stream<T, 64, 1>(a, st);
+  if constexpr (sizeof(T) == 2)
+    if (a.kv.D == 128 && wide) return launch_stream<T, 128, 2>(a, st);
+  return a.kv.D == 128 ? launch_stream<T, 128, 1>(a, st) : launch_stream<T, 256, 1>(a, st);
 }
 
 }  // namespace
 
-size_t kv_attend_workspace(int) { return 16; }
+size_t kv_attend_workspace(int head_dim) {
+  const int rows = head_dim == 256 ? 8 : 16;
+  return (size_t)2 * kMaxCtas * rows * (head_dim + 2) * sizeof(float);
+}
 
 cudaError_t launch_kv_attend(const KvAttend& a, cudaStream_t st) {
   switch (a.dtype) {

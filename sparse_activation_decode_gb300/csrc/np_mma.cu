@@ -721,6 +721,20 @@ cudaError_t make_row_maps(RowMaps* out, const void* base, int dtype, uint64_t ro
   return cudaSuccess;
 }
 
+cudaError_t make_page_map(CUtensorMap* out, const void* base, int dim, uint64_t blocks) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return cudaErrorNotSupported;
+  const cuuint64_t dims[3] = {(cuuint64_t)dim, 64, blocks};
+  const cuuint64_t strides[2] = {(cuuint64_t)dim, (cuuint64_t)dim * 64};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {(cuuint32_t)(dim < 128 ? dim : 128), 64, 1};
+  const CUresult r = fn(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        dim < 128 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 size_t mma_smem_bytes(int mode, int ks_len, int n_stages) {
   const uint32_t stage = (mode == kMmaFfnGated || mode == kMmaFfnUp) ? 32768u : 16384u;
   return 1024 + kSmemHeader + (size_t)(ks_len / 64) * 2048 + (size_t)n_stages * stage;
