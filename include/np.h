@@ -399,7 +399,7 @@ typedef struct {
   void* k;            /* e4m3 [n_layers][n_pages][n_kv_heads][NP_KV_PAGE][head_dim] */
   void* v;            /* e4m3 [n_layers][n_pages][n_kv_heads][head_dim][NP_KV_PAGE] (transposed: the
                          product with the softmax weights then reads contiguous tokens) */
-  float* k_scale;     /* [n_layers][n_pages][n_kv_heads]: value = code * scale */
+  float* k_scale;     /* [n_layers][n_pages][n_kv_heads]: value = code * scale, 2^-40 <= scale <= 2^40 */
   float* v_scale;
   int32_t* table;     /* [max_seqs][max_pages] page numbers, -1 where there is none */
   int32_t* lengths;   /* [max_seqs] tokens held */
@@ -492,9 +492,10 @@ typedef struct {
 np_status np_kv_attend(const np_kv_desc* kv, int32_t layer, const np_kv_batch* batch, const np_kv_attn* attn,
                        void* stream);
 
-/* Bytes of workspace that any np_kv_attend on this cache needs; -1 for a
- * description that the calls would refuse. */
-int64_t np_kv_attend_workspace(const np_kv_desc* kv);
+/* Bytes of workspace that np_kv_attend needs for n_heads query heads of
+ * `dtype` and at most max_tokens new tokens per sequence (np_kv_batch
+ * .max_tokens) on the current device; -1 for arguments it would refuse. */
+int64_t np_kv_attend_workspace(const np_kv_desc* kv, int32_t n_heads, int32_t max_tokens, int32_t dtype);
 
 /* Synchronise `stream`, then read and clear the cache's error word:
  * NP_ERR_OOM (no free page left), NP_ERR_STATE (a row, length, page or token

@@ -99,7 +99,7 @@ SIGNATURES = {
     "np_ffn_rows_noalloc": (_I32, [_P, _P, _P, _P, _P, _I32, _I32, _I32, _I32, _I32, _P, _P]),
     "np_ffn_rows_noalloc_check": (_I32, [_P]),
     "np_kv_work_words": (_I64, [_P]),
-    "np_kv_attend_workspace": (_I64, [_P]),
+    "np_kv_attend_workspace": (_I64, [_P, _I32, _I32, _I32]),
     "np_kv_reserve": (_I32, [_P, _P, _P, _I32, _P]),
     "np_kv_fork": (_I32, [_P, _P, _P, _I32, _P]),
     "np_kv_release": (_I32, [_P, _P, _I32, _I32, _I32, _P]),

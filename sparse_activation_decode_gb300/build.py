@@ -20,7 +20,7 @@ LIB = os.path.join(HERE, "libnp.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["np_api.cu", "np_ffn.cu", "np_pred.cu", "np_set.cu", "np_scatter.cu", "np_noalloc.cu", "np_mma.cu",
-           "np_kv.cu", "np_kv_attend.cu"]
+           "np_kv.cu", "np_kv_attend.cu", "np_kv_tile.cu"]
 
 
 def _nvcc() -> str:

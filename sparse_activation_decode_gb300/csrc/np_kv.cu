@@ -677,8 +677,11 @@ extern "C" int64_t np_kv_work_words(const np_kv_desc* d) {
          (int64_t)d->max_seqs * d->max_pages;
 }
 
-extern "C" int64_t np_kv_attend_workspace(const np_kv_desc* d) {
-  return shape_ok(d) ? (int64_t)kv_attend_workspace(d->head_dim) : -1;
+extern "C" int64_t np_kv_attend_workspace(const np_kv_desc* d, int32_t n_heads, int32_t max_tokens, int32_t dtype) {
+  if (!shape_ok(d) || n_heads < 1 || n_heads > 1024 || n_heads % d->n_kv_heads || max_tokens < 0 || dtype < NP_F32 ||
+      dtype > NP_BF16)
+    return -1;
+  return (int64_t)kv_attend_workspace(dtype, d->head_dim, (long long)max_tokens * (n_heads / d->n_kv_heads));
 }
 
 extern "C" np_status np_kv_reserve(const np_kv_desc* d, const int32_t* seqs, const int32_t* n_new, int32_t n,
@@ -771,7 +774,8 @@ extern "C" np_status np_kv_attend(const np_kv_desc* d, int32_t layer, const np_k
       t->q_head_stride < 0 || t->out_token_stride < 0 || t->out_head_stride < 0)
     return kv_fail(NP_ERR_ARG, "np_kv_attend: bad tensors");
   if (!t->workspace || !aligned(t->workspace, 16) ||
-      t->workspace_bytes < (int64_t)kv_attend_workspace(d->head_dim))
+      t->workspace_bytes <
+          (int64_t)kv_attend_workspace(t->dtype, d->head_dim, (long long)b->max_tokens * (t->n_heads / d->n_kv_heads)))
     return kv_fail(NP_ERR_ARG, "np_kv_attend: workspace missing, unaligned or too small");
   KvAttend a{view_of(d, layer), batch_of(b), t->q, t->out, t->q_token_stride, t->q_head_stride,
              t->out_token_stride, t->out_head_stride, t->n_heads, t->dtype, t->scale * 1.4426950408889634f,

@@ -81,8 +81,15 @@ struct KvAttend {
   int window, sinks;
   void* ws;
 };
-size_t kv_attend_workspace(int head_dim);
+// `rows`: the most rows (new tokens x query heads per key head) of a sequence.
+size_t kv_attend_workspace(int dtype, int head_dim, long long rows);
 cudaError_t launch_kv_attend(const KvAttend& a, cudaStream_t st);
+int kv_attend_ctas();  // CTAs of an attention launch: one per SM; 0 without a device
+
+// The tiled kernel (np_kv_tile.cu).
+bool kv_tile_takes(int dtype, int head_dim);
+size_t kv_tile_workspace(int dtype, int head_dim);
+cudaError_t launch_kv_tile(const KvAttend& a, cudaStream_t st);
 
 // Generic 16-bit / 32-bit element access.
 template <typename T> __device__ __forceinline__ float kv_to_float(T v);

@@ -50,6 +50,7 @@ namespace {
 
 constexpr int kMaxCtas = 256;       // upper bound of the grid (workspace)
 constexpr int kMaxAttendStages = 16;
+constexpr int kTileRows = 16;       // sequences with more rows go to the tiled kernel
 constexpr int kWholePages = 8;      // items of at most this many pages are never cut
 
 template <int D> struct Shape {
@@ -711,7 +712,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(256) attend_join_kernel(const KvAttend a, int ctas) {
   constexpr int R = 8 * NT;
-  extern __shared__ __align__(16) uint8_t smem_raw[];
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ long long tmp[2];
   long long* pre = reinterpret_cast<long long*>(smem_raw);
   SeqWork* seq = reinterpret_cast<SeqWork*>(pre + a.batch.n_seqs + 1 + ((a.batch.n_seqs + 1) & 1));
@@ -748,23 +749,14 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const KvAttend a, int 
   }
 }
 
-int sm_count() {
-  static int n[64] = {};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-  if (n[dev] == 0) cudaDeviceGetAttribute(&n[dev], cudaDevAttrMultiProcessorCount, dev);
-  return n[dev];
-}
-
 template <typename T, int D, int NT> struct StreamTag {};
 
 template <typename T, int D, int NT>
 cudaError_t launch_stream(const KvAttend& a, cudaStream_t st) {
   using Sh = Shape<D>;
   constexpr int R = 8 * NT;
-  int ctas = sm_count();
+  const int ctas = kv_attend_ctas();
   if (ctas < 1) return cudaErrorInvalidDevice;
-  if (ctas > kMaxCtas) ctas = kMaxCtas;
   CUtensorMap map;
   const cudaError_t me = make_page_map(&map, a.kv.k, D, (uint64_t)a.kv.n_pages * a.kv.H);
   if (me != cudaSuccess) return me;
@@ -805,12 +797,26 @@ cudaError_t launch_typed(const KvAttend& a, cudaStream_t st) {
 
 }  // namespace
 
-size_t kv_attend_workspace(int head_dim) {
-  const int rows = head_dim == 256 ? 8 : 16;
-  return (size_t)2 * kMaxCtas * rows * (head_dim + 2) * sizeof(float);
+int kv_attend_ctas() {
+  static int n[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  if (n[dev] == 0) cudaDeviceGetAttribute(&n[dev], cudaDevAttrMultiProcessorCount, dev);
+  return n[dev] < kMaxCtas ? n[dev] : kMaxCtas;
+}
+
+static bool takes_tile(int dtype, int head_dim, long long rows) {
+  return rows > kTileRows && kv_tile_takes(dtype, head_dim);
+}
+
+size_t kv_attend_workspace(int dtype, int head_dim, long long rows) {
+  const size_t stream = (size_t)2 * kMaxCtas * (head_dim == 256 ? 8 : 16) * (head_dim + 2) * sizeof(float);
+  const size_t tile = takes_tile(dtype, head_dim, rows) ? kv_tile_workspace(dtype, head_dim) : 0;
+  return stream > tile ? stream : tile;
 }
 
 cudaError_t launch_kv_attend(const KvAttend& a, cudaStream_t st) {
+  if (takes_tile(a.dtype, a.kv.D, (long long)a.batch.max_tokens * (a.Hq / a.kv.H))) return launch_kv_tile(a, st);
   switch (a.dtype) {
     case 0: return launch_typed<float>(a, st);
     case 1: return launch_typed<__half>(a, st);

@@ -87,8 +87,7 @@ class KvCache:
         d.n_layers, d.n_pages, d.n_kv_heads, d.head_dim = n_layers, n_pages, heads, dim
         d.max_seqs, d.max_pages = self.max_seqs, self.max_pages
         words = self.lib.np_kv_work_words(ctypes.byref(d))
-        self._ws_bytes = self.lib.np_kv_attend_workspace(ctypes.byref(d))
-        if words < 0 or self._ws_bytes < 0:
+        if words < 0:
             raise ValueError("unsupported cache sizes: head_dim must be 64, 128 or 256, at most 256 heads")
         self._work = torch.zeros(words, dtype=torch.int32, device=self.device)
         d.k, d.v, d.k_scale, d.v_scale = k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr()
@@ -96,6 +95,7 @@ class KvCache:
                                               self._work.data_ptr())
         self.desc = d
         self._desc = ctypes.byref(d)
+        self._ws_bytes = {}  # workspace sizes by (heads, most new tokens, dtype)
 
     # -- argument checks -----------------------------------------------------
     def _stream(self) -> int:
@@ -196,9 +196,16 @@ class KvCache:
             if q.numel() and _spans_overlap(q, out):
                 raise ValueError("out may not share memory with q")
         b = self._batch(q.shape[0], cu, seqs, max_q)
-        ws = torch.empty(self._ws_bytes, dtype=torch.uint8, device=q.device)
+        key = (q.shape[1], b.max_tokens, q.dtype)
+        n_ws = self._ws_bytes.get(key)
+        if n_ws is None:
+            n_ws = self.lib.np_kv_attend_workspace(self._desc, q.shape[1], b.max_tokens, _DTYPES[q.dtype])
+            if n_ws < 0:
+                raise ValueError(f"{q.shape[1]} query heads over {self.n_kv_heads} key heads are not supported")
+            self._ws_bytes[key] = n_ws
+        ws = torch.empty(n_ws, dtype=torch.uint8, device=q.device)
         t = L.KvAttn(q.data_ptr(), out.data_ptr(), q.stride(0), q.stride(1), out.stride(0), out.stride(1),
-                     ws.data_ptr(), self._ws_bytes, q.shape[1], _DTYPES[q.dtype],
+                     ws.data_ptr(), n_ws, q.shape[1], _DTYPES[q.dtype],
                      1.0 / math.sqrt(self.head_dim) if scale is None else scale, window, sinks)
         L.check(self.lib.np_kv_attend(self._desc, layer, ctypes.byref(b), ctypes.byref(t), st), "np_kv_attend")
         return out

@@ -488,13 +488,13 @@ def test_wrapper_refuses_misuse():
               lambda: c.attend(0, q.transpose(1, 2)), lambda: c.attend(0, q, out=q),
               lambda: c.attend(0, q, out=torch.empty_like(q).float()), lambda: c.attend(0, q[:1], cu=None),
               lambda: c.attend(0, q, cu=torch.tensor([0, 1, 2])), lambda: c.attend(0, q, cu=i32([0, 2]).long()),
-              lambda: c.append(0, kv, kv[:1]), lambda: c.append(0, kv, kv.float()), lambda: c.append(0, q, q),
+              lambda: c.append(0, kv, kv[:1]), lambda: c.attend(0, q[:, :3].contiguous()), lambda: c.append(0, kv, kv.float()), lambda: c.append(0, q, q),
               lambda: c.reserve(i32([[1, 1]])), lambda: c.fork(i32([0]), i32([0, 1])),
               lambda: KvCache(n_layers=1, n_pages=2, n_kv_heads=1, head_dim=80, max_seqs=1, max_pages=1),
               lambda: KvCache.wrap(c.k, c.v, c.k_scale, c.v_scale, c.table, c.lengths, c.refs[:3])):
         with pytest.raises(ValueError):
             f()
-    for f in (lambda: c.attend(1, q), lambda: c.attend(0, q[:, :3].contiguous()), lambda: c.attend(0, q, scale=-1.0),
+    for f in (lambda: c.attend(1, q), lambda: c.attend(0, q, scale=-1.0),
               lambda: c.attend(0, q, window=-1), lambda: c.append(5, kv, kv), lambda: c.release(i32([0]), window=-3)):
         with pytest.raises(NpError):
             f()

@@ -42,7 +42,7 @@ def batch(**kw):
 
 
 def attn(lib, d=None, **kw):
-    ws = lib.np_kv_attend_workspace(ctypes.byref(d or desc()))
+    ws = lib.np_kv_attend_workspace(ctypes.byref(d or desc()), 8, 10, L.NP_F16)
     t = L.KvAttn(FAKE, 2 * FAKE, 8 * 128, 128, 8 * 128, 128, 4 * FAKE, ws, 8, L.NP_F16, 0.1, 0, 0)
     for k, v in kw.items():
         setattr(t, k, v)
@@ -124,7 +124,9 @@ def test_work_words_cover_every_list(lib):
     words = lib.np_kv_work_words(ctypes.byref(d))
     assert words >= 4 + 2 * max(d.n_pages // 2 + 1, d.max_seqs) + d.max_seqs + d.n_pages + d.max_seqs * d.max_pages
     assert lib.np_kv_work_words(ctypes.byref(desc(head_dim=80))) == -1
-    assert lib.np_kv_work_words(None) == -1 and lib.np_kv_attend_workspace(None) == -1
+    assert lib.np_kv_work_words(None) == -1 and lib.np_kv_attend_workspace(None, 8, 1, L.NP_F16) == -1
+    for heads, most, dtype in ((6, 1, L.NP_F16), (0, 1, L.NP_F16), (2048, 1, L.NP_F16), (8, -1, L.NP_F16), (8, 1, 3)):
+        assert lib.np_kv_attend_workspace(ctypes.byref(d), heads, most, dtype) == -1
 
 
 def test_cache_refuses_host_tensors_and_bad_sizes():
