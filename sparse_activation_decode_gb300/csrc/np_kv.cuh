@@ -91,6 +91,48 @@ bool kv_tile_takes(int dtype, int head_dim);
 size_t kv_tile_workspace(int dtype, int head_dim);
 cudaError_t launch_kv_tile(const KvAttend& a, cudaStream_t st);
 
+// Bounded wait for a phase of an mbarrier: gives up after about one second, or
+// when another thread of the CTA has set *abort; a timeout is recorded and
+// sets *abort.  The timer is read only after many failed looks: reading it
+// costs more than most waits last.
+__device__ __forceinline__ bool kv_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int* err) {
+  uint64_t t0 = 0;
+  for (uint32_t it = 1;; ++it) {
+    if (__builtin_expect(mbar_try_wait(bar, parity), 1)) return true;
+    if (__builtin_expect((it & 255u) == 0, 0)) {
+      if (*abort) return false;
+      const uint64_t t = global_ns();
+      if (t0 == 0) t0 = t;
+      if (t - t0 > kWaitLimitNs) {
+        atomicExch(err, kDevErrTimeout);
+        *abort = 1;
+        return false;
+      }
+    }
+  }
+}
+
+// Phase test that does not suspend the thread.
+__device__ __forceinline__ bool kv_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// Waits for two phases; where both are over already, their looks overlap
+// (one look takes 100 to 200 cycles).
+__device__ __forceinline__ bool kv_wait2(uint64_t* bar0, uint32_t parity0, uint64_t* bar1, uint32_t parity1,
+                                         volatile int* abort, int* err) {
+  const bool r0 = kv_test(bar0, parity0), r1 = kv_test(bar1, parity1);
+  return (r0 || kv_wait(bar0, parity0, abort, err)) && (r1 || kv_wait(bar1, parity1, abort, err));
+}
+
 // Generic 16-bit / 32-bit element access.
 template <typename T> __device__ __forceinline__ float kv_to_float(T v);
 template <> __device__ __forceinline__ float kv_to_float<float>(float v) { return v; }

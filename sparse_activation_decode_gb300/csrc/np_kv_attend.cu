@@ -279,11 +279,6 @@ struct StageMeta {
   float k_scale, v_scale;
 };
 
-// Wait for a phase unless the CTA has given up already.
-__device__ __forceinline__ bool wait_stage(uint64_t* bar, uint32_t parity, volatile int* abort, int* err) {
-  return wait_phase(smem_addr(bar), parity, abort, err);
-}
-
 // Wait for page i in stage st.  Pages land in any order and a stage's pages
 // belong to different warps, so a warp may come before the stage's previous
 // page has landed; the barrier's parity cannot tell that from its own page
@@ -291,20 +286,20 @@ __device__ __forceinline__ bool wait_stage(uint64_t* bar, uint32_t parity, volat
 // stage to itself again, after which the parity is unambiguous.
 __device__ __forceinline__ bool wait_page(volatile StageMeta* meta, uint64_t* bar, uint32_t i, uint32_t parity,
                                           volatile int* abort, int* err) {
-  if (meta->seq != i + 1) {
-    const uint64_t t0 = global_ns();
-    for (uint32_t it = 1; meta->seq != i + 1; ++it) {
-      if ((it & 127u) == 0) {
-        if (*abort) return false;
-        if (global_ns() - t0 > kWaitLimitNs) {
-          atomicExch(err, kDevErrTimeout);
-          *abort = 1;
-          return false;
-        }
+  uint64_t t0 = 0;
+  for (uint32_t it = 1; meta->seq != i + 1; ++it) {
+    if ((it & 255u) == 0) {
+      if (*abort) return false;
+      const uint64_t t = global_ns();
+      if (t0 == 0) t0 = t;
+      if (t - t0 > kWaitLimitNs) {
+        atomicExch(err, kDevErrTimeout);
+        *abort = 1;
+        return false;
       }
     }
   }
-  return wait_stage(bar, parity, abort, err);
+  return kv_wait(bar, parity, abort, err);
 }
 
 // Partials of cut items: slot 2c for a stretch of CTA c that continues an
@@ -390,7 +385,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
           const int pg = __shfl_sync(0xffffffffu, page, i), bs = __shfl_sync(0xffffffffu, base, i);
           const float ksi = __shfl_sync(0xffffffffu, ks, i), vsi = __shfl_sync(0xffffffffu, vs, i);
           const uint32_t st = count % ns;
-          if (count >= ns) alive = wait_stage(&empty[st], (count / ns - 1) & 1, &abort_s, a.kv.err);
+          if (count >= ns) alive = kv_wait(&empty[st], (count / ns - 1) & 1, &abort_s, a.kv.err);
           alive = __shfl_sync(0xffffffffu, (int)alive, 0) != 0;
           if (!alive) break;
           if (lane == 0) {

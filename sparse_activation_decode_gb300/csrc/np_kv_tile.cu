@@ -1,9 +1,9 @@
 // Attention over the 8-bit paged key/value cache, tiled kernel: prompts.
 //
 // Rows (new tokens x the query heads that share a key head) are taken R = 256
-// (or 128) at a time as one or two tiles of 128; a step is 128 keys, two
-// pages:   S = Q K^T (tcgen05, 128 x 128 x D),  weights,  O += P V (tcgen05,
-// 128 x D x 128), with S, P and O in tensor memory.  Q is fp16 after an exact
+// (or 128) at a time as one or two tiles of 128; a step is one page of 64
+// keys:   S = Q K^T (tcgen05, 128 x 64 x D),  weights P,  O += P V (tcgen05,
+// 128 x D x 64), with S, P and O in tensor memory.  Q is fp16 after an exact
 // scaling of each row by a power of two (fp32 queries: the sum of two fp16
 // parts), K and V are e4m3 widened exactly to fp16, P is fp16 (two parts for
 // fp32 outputs); sums, maxima and the accumulators are fp32.
@@ -12,17 +12,22 @@
 // goes into the weights, w = 2^(s - M + lv - LV) with lv = log2(v_scale) and
 // LV the unit that O is held in, so O needs no scaling per page; the softmax
 // sum takes w 2^(LV - lv).  When a page's lv is more than 3 away from LV, O
-// is multiplied (fp32) into the unit of that page, and pages whose scales are
-// further apart than that are never put into one step: a weight that fp16
-// cannot hold is below 2^-29 of its row's largest, whatever the scales.  M is
-// raised only when a row's maximum has grown by more than 2^4 since it was
-// set, so that O is seldom rescaled; weights carry a factor 2^8.
+// is multiplied (fp32) into the unit of that page: a weight that fp16 cannot
+// hold is below 2^-29 of its row's largest, whatever the scales.  M is raised
+// only when a row's maximum has grown by more than 2^4 since it was set, so
+// that O is seldom rescaled; weights carry a factor 2^8.  For fp32 outputs O
+// is added to a second accumulator every 8 steps: the tensor core's own adds
+// truncate, and over n of them their bias is n 2^-25.
 //
 // Roles (512 threads, one CTA per SM): warps 0-3 and 4-7 the softmax of tile
 // 0 and 1 (a thread per row, no exchange between threads), warps 8-11 widen
-// the pages from global memory into the swizzled operands, warp 12 issues
-// every MMA, warp 13 walks the work list and looks up pages and scales.  The
-// two tiles alternate: while one tile's softmax runs, the other's products do.
+// the pages from global memory into the swizzled operands, warps 12
+// and 14 issue the MMAs of tile 0 and 1, warp 13 walks the work list and looks
+// up pages and scales.  S is
+// held twice per tile: the products of the next page run while the weights of
+// this one are formed, so neither waits for the other's latency.  (With one S
+// of 128 keys per tile instead, a step's S -> weights -> P V -> S chain was
+// 6300 cycles for 4 x 512 cycles of products.)
 // Bound: the tensor cores, 4 D flops per visible (query head, key); next
 // shared memory (operands of S from both tiles, the widened pages' writes).
 //
@@ -44,26 +49,29 @@ namespace {
 
 constexpr int kTileThreads = 512;
 constexpr int kMetaSlots = 8;
-constexpr int kStepKeys = 128;
+constexpr int kStepKeys = 64;
+constexpr int kMaxBuffers = 4;
+constexpr int kFold = 8;  // steps between additions into the second accumulator (fp32 outputs)
 // log2 of: the growth a weight may show before M is raised, the distance of a
 // page's value scale from O's unit, the factor on all weights.  Together they
 // stay below fp16's largest, 2^16.
 constexpr float kLazy = 4.f, kUnit = 3.f, kLift = 8.f;
-constexpr int kCutCost = 8;    // steps that cutting an item costs (partials, second launch)
+constexpr int kCutCost = 16;   // steps that cutting an item costs (partials, second launch)
 
 // NX tiles of 128 rows, NP fp16 parts of Q and P, NB operand buffers.
 template <typename T, int D> struct TileShape {
   static constexpr int NP = sizeof(T) == 4 ? 2 : 1;
   static constexpr int NX = (D == 256 || NP == 2) ? 1 : 2;
-  static constexpr int NB = D == 256 ? 1 : 2;
+  static constexpr int NB = D == 256 ? 2 : 4;
   static constexpr int R = 128 * NX;
   static constexpr uint32_t kQ = 128 * D * 2;            // bytes of one part of one tile's Q
   static constexpr uint32_t kKV = kStepKeys * D * 2;     // bytes of one operand buffer
   static constexpr uint32_t kOperands = NX * NP * kQ + 2 * NB * kKV;
-  // tensor memory columns
+  // tensor memory columns: two S of 64 per tile (P takes the place of its S),
+  // then O, then for fp32 outputs the second accumulator
   static constexpr uint32_t S(int x) { return x * 128u; }
-  static constexpr uint32_t P(int x) { return NX == 2 ? x * 128u : 128u; }
   static constexpr uint32_t O(int x) { return 256u + x * (uint32_t)D; }
+  static constexpr uint32_t kAcc = 256u + D;
 };
 
 struct TileSeq {
@@ -79,7 +87,6 @@ struct TilePlan {
 struct TileKeys {
   int sink, lo, pages, p_min, p_max, rows;
   __device__ __forceinline__ int slot(int k) const { return k < sink ? k : lo + (k - sink); }
-  __device__ __forceinline__ int steps() const { return (pages + 1) >> 1; }
 };
 
 template <int R>
@@ -127,7 +134,7 @@ __device__ __forceinline__ TilePlan tile_plan(const KvAttend& a, int ctas, long 
     const int tiles = tiles_of(a, seq[i].n, R);
     int steps = 0, longest = 0;
     for (int t = lane; t < tiles; t += 32) {
-      const int s = tile_keys<R>(a, seq[i].n, seq[i].len, t).steps();
+      const int s = tile_keys<R>(a, seq[i].n, seq[i].len, t).pages;
       steps += s;
       longest = s > longest ? s : longest;
     }
@@ -214,7 +221,7 @@ __device__ __forceinline__ TilePos tile_find(const KvAttend& a, const TilePlan& 
   if (!p.split) return t;
   for (int base = 0; base < t.tiles; base += 32) {
     const int i = base + lane;
-    const int s = i < t.tiles ? tile_keys<R>(a, seq[lo].n, seq[lo].len, i).steps() : 0;
+    const int s = i < t.tiles ? tile_keys<R>(a, seq[lo].n, seq[lo].len, i).pages : 0;
     int x = s;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -234,31 +241,49 @@ __device__ __forceinline__ TilePos tile_find(const KvAttend& a, const TilePlan& 
   return t;
 }
 
-struct StepMeta {
-  int flags;     // 1: first of a stretch, 2: last, 4: no more work, 8: stretch starts its item, 16: ends it
-  int nx;        // tiles with rows
-  int page[2];   // -1: nothing
-  int base[2];   // position of the first token
-  float ks[2], lv[2];  // key scale, log2 of the value scale
+struct __align__(16) StepMeta {
+  // 1: first of a stretch, 2: last, 4: no more work, 8: stretch starts its
+  // item, 16: ends it; from bit 8 on: tiles with rows
+  int flags;
+  int base;      // position of the first token; -1: nothing
+  float ks, lv;  // key scale, log2 of the value scale
+  int page;      // -1: nothing
   int row0;      // first row of the item in its sequence and head
   int rows;
   int begin, n, len, h;
 };
 
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
-  uint32_t r[32];
+// 32 lanes x 64 consecutive fp32 columns.  v is valid after tmem_landed64,
+// which names every register so that no use can be moved in front of it.
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, float* v) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
+      "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+      "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+        "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]),
+        "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]),
+        "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31]),
+        "=f"(v[32]), "=f"(v[33]), "=f"(v[34]), "=f"(v[35]), "=f"(v[36]), "=f"(v[37]), "=f"(v[38]), "=f"(v[39]),
+        "=f"(v[40]), "=f"(v[41]), "=f"(v[42]), "=f"(v[43]), "=f"(v[44]), "=f"(v[45]), "=f"(v[46]), "=f"(v[47]),
+        "=f"(v[48]), "=f"(v[49]), "=f"(v[50]), "=f"(v[51]), "=f"(v[52]), "=f"(v[53]), "=f"(v[54]), "=f"(v[55]),
+        "=f"(v[56]), "=f"(v[57]), "=f"(v[58]), "=f"(v[59]), "=f"(v[60]), "=f"(v[61]), "=f"(v[62]), "=f"(v[63])
       : "r"(taddr)
       : "memory");
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_landed64(float* v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+      : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+        "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]),
+        "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]),
+        "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31]),
+        "+f"(v[32]), "+f"(v[33]), "+f"(v[34]), "+f"(v[35]), "+f"(v[36]), "+f"(v[37]), "+f"(v[38]), "+f"(v[39]),
+        "+f"(v[40]), "+f"(v[41]), "+f"(v[42]), "+f"(v[43]), "+f"(v[44]), "+f"(v[45]), "+f"(v[46]), "+f"(v[47]),
+        "+f"(v[48]), "+f"(v[49]), "+f"(v[50]), "+f"(v[51]), "+f"(v[52]), "+f"(v[53]), "+f"(v[54]), "+f"(v[55]),
+        "+f"(v[56]), "+f"(v[57]), "+f"(v[58]), "+f"(v[59]), "+f"(v[60]), "+f"(v[61]), "+f"(v[62]), "+f"(v[63])
+      :
+      : "memory");
 }
 
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
@@ -280,6 +305,38 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint
       : "memory");
 }
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n\t.reg .b64 ra, rb, rc;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmov.b64 rc, {%6, %7};\n\t"
+      "fma.rn.f32x2 ra, ra, rb, rc;\n\tmov.b64 {%0, %1}, ra;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 ra, rb;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "add.rn.f32x2 ra, ra, rb;\n\tmov.b64 {%0, %1}, ra;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+// One lane of a converged warp, the same every time.
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
+// Registers of a warpgroup after launch.
+template <int N> __device__ __forceinline__ void reg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N> __device__ __forceinline__ void reg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -292,9 +349,8 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
-__device__ __forceinline__ uint32_t no_nan(uint32_t v) {
-  const __half2 h = __hmin2(*reinterpret_cast<__half2*>(&v), __floats2half2_rn(448.f, 448.f));
-  return *reinterpret_cast<const uint32_t*>(&h);
+__device__ __forceinline__ void sts64(uint32_t addr, uint32_t a, uint32_t b) {
+  asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
 }
 
 // 16 bytes of T from floats.
@@ -316,7 +372,6 @@ template <> __device__ __forceinline__ uint4 pack_chunk<__nv_bfloat16>(const flo
 }
 
 // 16 codes as 16 fp16 values into two 16-byte chunks.
-template <bool CLEAN>
 __device__ __forceinline__ void widen16(const uint4& v, uint32_t a0, uint32_t a1) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   uint32_t f[8];
@@ -325,20 +380,24 @@ __device__ __forceinline__ void widen16(const uint4& v, uint32_t a0, uint32_t a1
     f[2 * i] = e4m3x2_to_f16x2(w[i] & 0xffffu);
     f[2 * i + 1] = e4m3x2_to_f16x2(w[i] >> 16);
   }
-  if constexpr (CLEAN) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = no_nan(f[i]);
-  }
   sts128(a0, f[0], f[1], f[2], f[3]);
   sts128(a1, f[4], f[5], f[6], f[7]);
 }
 
+// Codes that are NaN become 0.
+__device__ __forceinline__ uint32_t clean4(uint32_t w) { return w & ~__vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu); }
+
+// Code that few steps run goes out of the loops' way: the roles' loops together
+// have to stay in the instruction cache.
+__device__ __forceinline__ bool rare(bool c) { return __builtin_expect(c, 0); }
+
 struct TileShared {
   uint64_t meta_full[kMetaSlots], meta_empty[kMetaSlots];
-  uint64_t kfull[2], kempty[2], vfull[2], vempty[2];
-  uint64_t qready[2], sfull[2], pready[2], pvdone[2], drained;
+  uint64_t kfull[kMaxBuffers], kempty[kMaxBuffers], vfull[kMaxBuffers], vempty[kMaxBuffers];
+  uint64_t qready[2], sfull[2][2], pready[2][2], pvdone[2], drained[2];  // [tile][S buffer]
   StepMeta meta[kMetaSlots];
   long long tmp[3];
+  float fac[2][128];  // factor of each row's logits
   uint32_t tmem;
   int abort;
 };
@@ -367,19 +426,24 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const KvAt
   if (tid == 0) {
     for (int i = 0; i < kMetaSlots; ++i) {
       mbar_init(&sh.meta_full[i], 1);
-      mbar_init(&sh.meta_empty[i], 4 * NX + 4 + 1);
+      mbar_init(&sh.meta_empty[i], 4 * NX + 4 + NX);
+    }
+    for (int i = 0; i < kMaxBuffers; ++i) {
+      mbar_init(&sh.kfull[i], 4);
+      mbar_init(&sh.kempty[i], NX);
+      mbar_init(&sh.vfull[i], 4);
+      mbar_init(&sh.vempty[i], NX);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh.kfull[i], 4);
-      mbar_init(&sh.kempty[i], 1);
-      mbar_init(&sh.vfull[i], 4);
-      mbar_init(&sh.vempty[i], 1);
       mbar_init(&sh.qready[i], 4);
-      mbar_init(&sh.sfull[i], 1);
-      mbar_init(&sh.pready[i], 4);
       mbar_init(&sh.pvdone[i], 1);
+      for (int j = 0; j < 2; ++j) {
+        mbar_init(&sh.sfull[i][j], 1);
+        mbar_init(&sh.pready[i][j], 4);
+      }
     }
-    mbar_init(&sh.drained, 1);
+    mbar_init(&sh.drained[0], 1);
+    mbar_init(&sh.drained[1], 1);
     sh.abort = 0;
     fence_barrier_init();
   }
@@ -394,8 +458,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const KvAt
   const uint32_t tmem = sh.tmem;
   const int g = a.Hq / a.kv.H;
   volatile int* abort = &sh.abort;
-  auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_phase(smem_addr(bar), parity, abort, a.kv.err); };
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return kv_wait(bar, parity, abort, a.kv.err); };
 
+  // registers: 512 x 128 at launch = 256 x 168 + 256 x 88
+  if (warp >= 12) {
+    reg_dec<88>();
   if (warp == 13) {
     // ---- work list ----
     const long long u0 = (long long)blockIdx.x * p.chunk;
@@ -414,16 +481,16 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const KvAt
       for (long long u = u0; u < u1 && alive;) {
         const TileSeq w = seq[t.b];
         const TileKeys tk = tile_keys<R>(a, w.n, w.len, t.tile);
-        const int steps = tk.steps();
+        const int steps = tk.pages;
         const int s0 = t.step;
         int s1 = steps;
         if (p.split && (long long)(steps - s0) > u1 - u) s1 = s0 + (int)(u1 - u);
-        for (int sb = s0; sb < s1 && alive; sb += 16) {
-          // lane = page: the entries and scales of 16 steps at a time
-          const int k = 2 * sb + lane;
+        for (int sb = s0; sb < s1 && alive; sb += 32) {
+          // lane = step: the entries and scales of 32 pages at a time
+          const int k = sb + lane;
           int page = -1, base = -1;
           float ks = 0.f, vs = 1.f;
-          if (k < tk.pages && k < 2 * s1) {
+          if (k < s1) {
             const int slot = tk.slot(k);
             if (slot * kKvPage <= tk.p_max) {
               page = a.kv.table[(size_t)w.row * a.kv.max_pages + slot];
@@ -441,39 +508,29 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const KvAt
           // exact where the scale is a power of two
           const uint32_t vu = __float_as_uint(vs);
           const float lv = (vu & 0x7fffffu) == 0 ? (float)((int)(vu >> 23) - 127) : log2f(vs);
-          // steps whose two pages have scales too far apart become two
-          const float other = __shfl_xor_sync(0xffffffffu, lv, 1);
-          const int mate = __shfl_xor_sync(0xffffffffu, page, 1);
-          const unsigned apart = __ballot_sync(0xffffffffu, page >= 0 && mate >= 0 && fabsf(lv - other) > kUnit);
-          for (int i = 0; i < 16 && sb + i < s1; ++i) {
-            const int parts = (apart >> (2 * i)) & 1 ? 2 : 1;
-            for (int part = 0; part < parts; ++part) {
-              if (!slot_free()) break;
-              StepMeta* m = &sh.meta[count % kMetaSlots];
-              if ((lane >> 1) == i) {
-                const int x = lane & 1;
-                const bool here = parts == 1 || x == part;
-                m->page[x] = here ? page : -1;
-                m->base[x] = here ? base : -1;
-                m->ks[x] = ks;
-                m->lv[x] = lv;
-              }
-              if (lane == 0) {
-                const int s = sb + i;
-                m->flags = (s == s0 && part == 0 ? 1 : 0) | (s == s1 - 1 && part == parts - 1 ? 2 : 0) |
-                           (s0 == 0 ? 8 : 0) | (s1 == steps ? 16 : 0);
-                m->nx = (tk.rows + 127) / 128;
-                m->row0 = t.tile * R;
-                m->rows = tk.rows;
-                m->begin = w.begin;
-                m->n = w.n;
-                m->len = w.len;
-                m->h = t.h;
-              }
-              __syncwarp();
-              if (lane == 0) mbar_arrive_local(smem_addr(&sh.meta_full[count % kMetaSlots]));
-              ++count;
+          for (int i = 0; i < 32 && sb + i < s1; ++i) {
+            if (!slot_free()) break;
+            StepMeta* m = &sh.meta[count % kMetaSlots];
+            if (lane == i) {
+              m->page = page;
+              m->base = base;
+              m->ks = ks;
+              m->lv = lv;
             }
+            if (lane == 0) {
+              const int s = sb + i;
+              m->flags = (s == s0 ? 1 : 0) | (s == s1 - 1 ? 2 : 0) | (s0 == 0 ? 8 : 0) | (s1 == steps ? 16 : 0) |
+                         ((tk.rows + 127) / 128) << 8;
+              m->row0 = t.tile * R;
+              m->rows = tk.rows;
+              m->begin = w.begin;
+              m->n = w.n;
+              m->len = w.len;
+              m->h = t.h;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive_local(smem_addr(&sh.meta_full[count % kMetaSlots]));
+            ++count;
           }
         }
         u += p.split ? s1 - s0 : 1;
@@ -497,430 +554,513 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const KvAt
         mbar_arrive_local(smem_addr(&sh.meta_full[count % kMetaSlots]));
       }
     }
-  } else if (warp == 12) {
-    // ---- MMA issue: one thread ----
-    if (lane == 0) {
-      constexpr uint32_t id_qk = idesc_f16(false, false, 128, kStepKeys);
-      constexpr uint32_t id_pv = idesc_f16(false, false, 128, D);
-      uint32_t mcount = 0, n_pv[2] = {0, 0}, n_q[2] = {0, 0}, steps = 0;
-      int flags = 4, nx = 0;
-      auto next_meta = [&](int& f, int& x) {
-        const uint32_t st = mcount % kMetaSlots;
-        if (!wait(&sh.meta_full[st], (mcount / kMetaSlots) & 1)) return false;
-        f = sh.meta[st].flags;
-        x = sh.meta[st].nx;
-        mbar_arrive_local(smem_addr(&sh.meta_empty[st]));
-        ++mcount;
-        return true;
-      };
-      // S of tile x for step `i` (of this CTA)
-      auto issue_qk = [&](int x, uint32_t i, bool first, bool last_tile) {
-        const uint32_t kb = i % NB;
-        if (x == 0 && !wait(&sh.kfull[kb], (i / NB) & 1)) return false;
-        if (n_pv[x] && !wait(&sh.pvdone[x], (n_pv[x] - 1) & 1)) return false;
-        if (first && !wait(&sh.qready[x], n_q[x]++ & 1)) return false;
-        tc_fence_after();
-#pragma unroll
-        for (int pt = 0; pt < NP; ++pt)
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t off = (k >> 2) * 16384u + (k & 3) * 32u;
-            tc_mma(tmem + Sh::S(x), smem_desc_sw128(q_s + (x * NP + pt) * Sh::kQ + off, 0, 1024),
-                   smem_desc_sw128(k_s + kb * Sh::kKV + off, 0, 1024), id_qk, pt || k);
+  } else if (warp == 12 || (NX == 2 && warp == 14)) {
+    // ---- MMA issue, one warp per tile ----
+    // The warp runs as one (every value the same in all lanes, taken through
+    // a reduction where it comes from memory) so that descriptors stay in
+    // uniform registers; the elected lane issues.  From divergent code each
+    // MMA took 75-100 cycles to issue, more than it takes to run.
+    constexpr uint32_t id_qk = idesc_f16(false, false, 128, kStepKeys);
+    constexpr uint32_t id_pv = idesc_f16(false, false, 128, D);
+    const uint32_t x = __reduce_max_sync(0xffffffffu, warp == 14);
+    const uint32_t tm = __reduce_max_sync(0xffffffffu, tmem);
+    const uint32_t t_s0 = tm + Sh::S(0) + x * 128, t_o = tm + Sh::O(0) + x * D;
+    const uint64_t qd = smem_desc_sw128(q_s + x * NP * Sh::kQ, 0, 1024), kd = smem_desc_sw128(k_s, 0, 1024),
+                   vd = smem_desc_sw128(v_s, 0, 1024);
+    const bool leader = elect_lane();
+    uint32_t step = 0;                  // the one whose S comes next
+    uint32_t n_s = 0, n_pv = 0, n_q = 0;  // S, P V issued, stretches begun
+    uint32_t in_stretch = 0;            // number of the current step in its stretch
+    bool mine = false, ok = true;       // the current step has rows in this tile
+    // flags of the next step, read ahead
+    auto read_flags = [&](uint32_t i) {
+      const uint32_t st = i % kMetaSlots;
+      const uint32_t f = __reduce_or_sync(0xffffffffu, (uint32_t)sh.meta[st].flags);
+      if (leader) mbar_arrive_local(smem_addr(&sh.meta_empty[st]));
+      return f;
+    };
+    ok = __all_sync(0xffffffffu, wait(&sh.meta_full[0], 0));
+    uint32_t nf = ok ? read_flags(0) : 4u;
+    for (;;) {
+      const bool end = nf & 4;
+      const bool next_mine = !end && x < nf >> 8;
+      uint32_t nnf = 0;                 // flags of the step after the next
+      // within a stretch: S of the next step, then P V of this one; where a
+      // stretch ends the product comes first, since the next one's queries
+      // wait for its result to be taken
+      const bool turn = nf & 5;
+#pragma unroll 1
+      for (int o = 0; o < 2; ++o) {
+        if ((o == 0) == turn) {
+          if (step == 0) continue;
+          const uint32_t i = step - 1, vb = i % NB, buf = n_pv & 1;
+          // (every step's phase is waited for, rows or not: parity tells
+          // only the last two phases apart)
+          if (mine)
+            ok = kv_wait2(&sh.vfull[vb], (i / NB) & 1, &sh.pready[x][buf], (n_pv >> 1) & 1, abort, a.kv.err);
+          else
+            ok = wait(&sh.vfull[vb], (i / NB) & 1);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          if (!mine) {
+            if (leader) mbar_arrive_local(smem_addr(&sh.vempty[vb]));
+            continue;
           }
-        tc_commit(smem_addr(&sh.sfull[x]));
-        if (last_tile) tc_commit(smem_addr(&sh.kempty[kb]));
-        return true;
-      };
-      auto issue_pv = [&](int x, uint32_t i, bool first, bool last_tile) {
-        const uint32_t vb = i % NB;
-        if (x == 0 && !wait(&sh.vfull[vb], (i / NB) & 1)) return false;
-        if (!wait(&sh.pready[x], n_pv[x] & 1)) return false;
-        tc_fence_after();
+          tc_fence_after();
+          const uint64_t bd = vd + ((vb * Sh::kKV) >> 4);
+          const uint32_t fresh = NP == 2 ? in_stretch % kFold == 0 : in_stretch == 0;
+          if (leader) {
 #pragma unroll
-        for (int pt = 0; pt < NP; ++pt)
+            for (int pt = 0; pt < NP; ++pt)
 #pragma unroll
-          for (int k = 0; k < kStepKeys / 16; ++k)
-            tc_mma_ts(tmem + Sh::O(x), tmem + Sh::P(x) + pt * 64 + k * 8,
-                      smem_desc_sw128(v_s + vb * Sh::kKV + (k >> 2) * (D * 128u) + (k & 3) * 32u, 0, 1024), id_pv,
-                      !first || pt || k);
-        tc_commit(smem_addr(&sh.pvdone[x]));
-        if (last_tile) tc_commit(smem_addr(&sh.vempty[vb]));
-        ++n_pv[x];
-        return true;
-      };
-      bool ok = next_meta(flags, nx);
-      if (ok && !(flags & 4))
-        for (int x = 0; x < nx && ok; ++x) ok = issue_qk(x, 0, true, x == nx - 1);
-      while (ok && !(flags & 4)) {
-        int nf = 4, nnx = 0;
-        ok = next_meta(nf, nnx);
-        if (!ok) break;
-        const bool more = !(nf & 4), fresh = (nf & 1) != 0;
-        if (more && !fresh) {
-          for (int x = 0; x < nx && ok; ++x) {
-            ok = issue_pv(x, steps, flags & 1, x == nx - 1);
-            if (ok) ok = issue_qk(x, steps + 1, false, x == nx - 1);
+              for (int k = 0; k < kStepKeys / 16; ++k)
+                tc_mma_ts(t_o, t_s0 + buf * 64 + pt * 32 + k * 8, bd + ((k * 32u) >> 4), id_pv,
+                          (fresh ^ 1) | (pt || k));
+            tc_commit(smem_addr(&sh.pvdone[x]));
+            tc_commit(smem_addr(&sh.vempty[vb]));
           }
+          __syncwarp();
+          ++n_pv;
         } else {
-          // a stretch ends here: both tiles' products first, since the next
-          // stretch's queries come only after their results were taken
-          for (int x = 0; x < nx && ok; ++x) ok = issue_pv(x, steps, flags & 1, x == nx - 1);
-          if (more)
-            for (int x = 0; x < nnx && ok; ++x) ok = issue_qk(x, steps + 1, true, x == nnx - 1);
+          if (end) continue;
+          const uint32_t kb = step % NB, buf = n_s & 1;
+          // the weights that lie in this S were read by the last P V issued (or one before it)
+          if (next_mine && n_pv)
+            ok = kv_wait2(&sh.kfull[kb], (step / NB) & 1, &sh.pvdone[x], (n_pv - 1) & 1, abort, a.kv.err);
+          else
+            ok = wait(&sh.kfull[kb], (step / NB) & 1);
+          if (next_mine && (nf & 1)) ok = ok && wait(&sh.qready[x], n_q++ & 1);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          if (!next_mine) {
+            if (leader) mbar_arrive_local(smem_addr(&sh.kempty[kb]));
+          } else {
+            tc_fence_after();
+            const uint64_t bd = kd + ((kb * Sh::kKV) >> 4);
+            if (leader) {
+#pragma unroll
+              for (int pt = 0; pt < NP; ++pt)
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k)
+                  tc_mma(t_s0 + buf * 64, qd + ((pt * Sh::kQ + (k >> 2) * 16384u + (k & 3) * 32u) >> 4),
+                         bd + (((k >> 2) * 8192u + (k & 3) * 32u) >> 4), id_qk, pt || k);
+              tc_commit(smem_addr(&sh.sfull[x][buf]));
+              tc_commit(smem_addr(&sh.kempty[kb]));
+            }
+            __syncwarp();
+            ++n_s;
+          }
+          // while these run
+          ok = __all_sync(0xffffffffu, wait(&sh.meta_full[(step + 1) % kMetaSlots], ((step + 1) / kMetaSlots) & 1));
+          if (!ok) break;
+          nnf = read_flags(step + 1);
         }
-        flags = nf;
-        nx = nnx;
-        ++steps;
       }
-      // nothing of this CTA may be in flight when it frees the tensor memory
-      tc_commit(smem_addr(&sh.drained));
-      const uint64_t t0 = global_ns();
-      while (!mbar_try_wait(&sh.drained, 0))
-        if (global_ns() - t0 > kWaitLimitNs) break;
+      if (!ok || end) break;
+      in_stretch = nf & 1 ? 0 : in_stretch + 1;
+      mine = next_mine;
+      nf = nnf;
+      ++step;
     }
+    // nothing of this CTA may be in flight when it frees the tensor memory
+    if (leader) tc_commit(smem_addr(&sh.drained[x]));
     __syncwarp();
-  } else if (warp >= 8 && warp < 12) {
-    // ---- widening: units K(0), V(0), K(1), V(1), .. ----
+    const uint64_t t0 = global_ns();
+    while (!mbar_try_wait(&sh.drained[x], 0))
+      if (global_ns() - t0 > kWaitLimitNs) break;
+  }
+  } else if (warp >= 8) {
+    reg_dec<88>();
+    // ---- widening ----
     const int ct = tid - 256;
     constexpr int CH = D / 16;                       // 16-byte chunks of a token's keys
-    constexpr int PER_PAGE = kKvPage * CH / 128;     // chunks per thread of one page
-    constexpr int NC = D == 256 ? PER_PAGE : 2 * PER_PAGE;  // chunks in flight per thread
-    constexpr int PIECES = 2 * PER_PAGE / NC;
+    constexpr int NC = kKvPage * CH / 128;           // chunks per thread of one page
     // place of a thread's c-th chunk of a page: eight neighbouring lanes hold
     // two rows x four chunks, whose fp16 images meet no bank twice
     const int qd = lane >> 3, l8 = lane & 7;
     const int k_ch = (qd % (D / 64)) * 4 + (l8 & 3), k_tok = (qd / (D / 64)) * 2 + (l8 >> 2);
     const int cw = ct >> 5;
     constexpr int TOK_W = 32 / CH;                   // tokens per warp and chunk index
-    uint4 buf[NC];
-    auto load = [&](const StepMeta& m, int side, int piece) {
+    uint4 kbuf[NC], vbuf[NC];
+    auto load = [&](uint4* buf, int page, int h, int side) {
+      const size_t block = (size_t)page * a.kv.H + h;
+      const uint8_t* src = (side ? a.kv.v + ct * 16 : a.kv.k + (cw * TOK_W + k_tok) * D + k_ch * 16) + block * kKvPage * D;
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
-        const int all = piece * NC + c, half = all / PER_PAGE, i = all % PER_PAGE;
-        const int page = m.page[half];
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (page >= 0) {
-          const size_t block = (size_t)page * a.kv.H + m.h;
-          const uint8_t* src = (side ? a.kv.v : a.kv.k) + block * kKvPage * D;
-          src += side ? (i * 128 + ct) * 16 : ((i * 4 + cw) * TOK_W + k_tok) * D + k_ch * 16;
-          v = *reinterpret_cast<const uint4*>(src);
-        }
-        buf[c] = v;
+        buf[c] = make_uint4(0, 0, 0, 0);
+        if (page >= 0) buf[c] = *reinterpret_cast<const uint4*>(src + c * (side ? 2048 : 4 * TOK_W * D));
       }
     };
-    auto store = [&](uint32_t dst, int side, int piece, int tail) {
+    auto store = [&](uint4* buf, uint32_t dst, int side, bool tail) {
+      if (side == 1 && rare(tail)) {  // bytes behind the end of a sequence may be anything
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+          buf[c] = make_uint4(clean4(buf[c].x), clean4(buf[c].y), clean4(buf[c].z), clean4(buf[c].w));
+      }
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
-        const int all = piece * NC + c, half = all / PER_PAGE, i = all % PER_PAGE;
-        if (side == 0) {
-          const int t = half * kKvPage + (i * 4 + cw) * TOK_W + k_tok;
-          const uint32_t row = dst + (k_ch >> 2) * 16384u + t * 128u;
-          const int ck = (k_ch & 3) * 2;
-          widen16<false>(buf[c], row + ((ck ^ (t & 7)) << 4), row + (((ck + 1) ^ (t & 7)) << 4));
-        } else {
-          const int d = (i * 128 + ct) >> 2, ck = ((i * 128 + ct) & 3) * 2;
-          const uint32_t row = dst + half * (D * 128u) + d * 128u;
-          const uint32_t a0 = row + ((ck ^ (d & 7)) << 4), a1 = row + (((ck + 1) ^ (d & 7)) << 4);
-          if (tail) widen16<true>(buf[c], a0, a1);  // bytes behind the end may be NaN
-          else widen16<false>(buf[c], a0, a1);
-        }
+        // row of the operand (token or element), its 64-column block, its 16-byte chunk
+        const int r = side ? (c * 128 + ct) >> 2 : (c * 4 + cw) * TOK_W + k_tok;
+        const int ck = (side ? ct & 3 : k_ch & 3) * 2;
+        const uint32_t row = dst + (side ? 0u : (k_ch >> 2) * 8192u) + r * 128u;
+        widen16(buf[c], row + ((ck ^ (r & 7)) << 4), row + (((ck + 1) ^ (r & 7)) << 4));
       }
     };
     bool alive = true;
-    auto read_meta = [&](uint32_t i, StepMeta& m) {
+    // page, head and whether the page holds the end of its sequence; false: no more
+    auto read_meta = [&](uint32_t i, int& page, int& h, bool& tail) {
       const uint32_t st = i % kMetaSlots;
       alive = alive && wait(&sh.meta_full[st], (i / kMetaSlots) & 1);
       alive = __all_sync(0xffffffffu, alive);
       if (!alive) return false;
-      m.flags = sh.meta[st].flags;
-      m.page[0] = sh.meta[st].page[0];
-      m.page[1] = sh.meta[st].page[1];
-      m.base[0] = sh.meta[st].base[0];
-      m.base[1] = sh.meta[st].base[1];
-      m.h = sh.meta[st].h;
-      m.len = sh.meta[st].len;
+      const int flags = sh.meta[st].flags;
+      page = sh.meta[st].page;
+      h = sh.meta[st].h;
+      tail = sh.meta[st].base + kKvPage > sh.meta[st].len;
       __syncwarp();
       if (lane == 0) mbar_arrive_local(smem_addr(&sh.meta_empty[st]));
-      return (m.flags & 4) == 0;
+      return (flags & 4) == 0;
     };
-    StepMeta m{};
-    bool any = read_meta(0, m);
-    if (any) load(m, 0, 0);
-    for (uint32_t i = 0; any; ++i) {
-      StepMeta nm{};
-      bool more = false;
-      const uint32_t b = i % NB;
-      const int tail = m.base[0] + kKvPage > m.len || m.base[1] + kKvPage > m.len;
-#pragma unroll
-      for (int side = 0; side < 2; ++side) {
-        uint64_t* empty = side ? &sh.vempty[b] : &sh.kempty[b];
-        if (i >= NB) alive = alive && wait(empty, (i / NB - 1) & 1);
-        alive = __all_sync(0xffffffffu, alive);
-        if (!alive) break;
-#pragma unroll
-        for (int piece = 0; piece < PIECES; ++piece) {
-          store((side ? v_s : k_s) + b * Sh::kKV, side, piece, tail);
-          // the next piece's codes are on their way while the others work
-          if (piece + 1 < PIECES) load(m, side, piece + 1);
-          else if (side == 0) load(m, 1, 0);
-          else {
-            more = read_meta(i + 1, nm);
-            if (more) load(nm, 0, 0);
-          }
-        }
-        fence_proxy_async_cta();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_local(smem_addr(side ? &sh.vfull[b] : &sh.kfull[b]));
-      }
-      if (!alive) break;
-      m = nm;
-      any = more;
+    // each side's codes of the next step are fetched as soon as its registers
+    // are free, while the other side is widened
+    int page = -1, h = 0;
+    bool tail = false;
+    bool any = read_meta(0, page, h, tail);
+    if (any) {
+      load(kbuf, page, h, 0);
+      load(vbuf, page, h, 1);
     }
-  } else if (warp < 4 * NX) {
+    for (uint32_t i = 0; any; ++i) {
+      const uint32_t b = i % NB;
+      const bool this_tail = tail;
+      if (i >= NB) alive = alive && wait(&sh.kempty[b], (i / NB - 1) & 1);
+      alive = __all_sync(0xffffffffu, alive);
+      if (!alive) break;
+      store(kbuf, k_s + b * Sh::kKV, 0, false);
+      fence_proxy_async_cta();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_local(smem_addr(&sh.kfull[b]));
+      any = read_meta(i + 1, page, h, tail);
+      if (any) load(kbuf, page, h, 0);
+      if (i >= NB) alive = alive && wait(&sh.vempty[b], (i / NB - 1) & 1);
+      alive = __all_sync(0xffffffffu, alive);
+      if (!alive) break;
+      store(vbuf, v_s + b * Sh::kKV, 1, this_tail);
+      fence_proxy_async_cta();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_local(smem_addr(&sh.vfull[b]));
+      if (any) load(vbuf, page, h, 1);
+    }
+  } else {
+    reg_inc<168>();
+    if (warp < 4 * NX) {
     // ---- softmax: a thread per row ----
     const int X = warp >> 2;
-    const int row = tid & 127;                             // row of the tile = lane of tensor memory
+    const int row = tid & 127;                                   // row of the tile = lane of tensor memory
     const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);  // (32 * warp) << 16
-    const uint32_t t_s = lanes + Sh::S(X), t_p = lanes + Sh::P(X), t_o = lanes + Sh::O(X);
+    const uint32_t t_o = lanes + Sh::O(X), t_acc = lanes + Sh::kAcc;
+    int in_stretch = 0;
     uint32_t mcount = 0, n_steps = 0;
     float ref = -INFINITY, l = 0.f, fac = 0.f;
-    float unit = 0.f;       // log2 of the unit of O
-    bool has_unit = false;
+    float unit = NAN;       // log2 of the unit of O; NaN: none yet
+    int w_min = 0, w_max = 0;  // positions of the warp's rows
     int pos = -1;
-    bool alive = true;
-    for (;;) {
-      const uint32_t st = mcount % kMetaSlots;
-      alive = wait(&sh.meta_full[st], (mcount / kMetaSlots) & 1);
-      alive = __all_sync(0xffffffffu, alive);
-      if (!alive) break;
-      const StepMeta m = sh.meta[st];
+    bool alive = true, in = false;
+    T* out = nullptr;       // this row's place in the output
+    // The head of the next step's entry.  An entry that begins a stretch is
+    // kept until the stretch does (it says where its rows are).
+    auto free_entry = [&]() {
       __syncwarp();
-      if (lane == 0) mbar_arrive_local(smem_addr(&sh.meta_empty[st]));
+      if (lane == 0) mbar_arrive_local(smem_addr(&sh.meta_empty[mcount % kMetaSlots]));
       ++mcount;
-      if (m.flags & 4) break;
-      if (X >= m.nx) continue;
-      const int at = m.row0 + X * 128 + row;               // row of the sequence and head
-      const bool in = X * 128 + row < m.rows;
-      const int tok = at / g, head = m.h * g + at % g;
-      if (m.flags & 1) {
-        // this row's query, scaled so that its largest element is in [2^14, 2^15)
-        const T* q = static_cast<const T*>(a.q) + (long long)(m.begin + tok) * a.q_tok + (long long)head * a.q_head;
-        const bool wide_ok = (reinterpret_cast<uintptr_t>(q) & 15) == 0;
-        float top = 0.f;
-        constexpr int E = Elem<T>::E;
-        for (int pass = 0; pass < 2; ++pass) {
-          float up = 1.f;
-          if (pass) {
-            int e = (int)(__float_as_uint(top) >> 23) - 127;
-            e = e < -112 ? -112 : e;
-            up = __uint_as_float((uint32_t)(14 - e + 127) << 23);
-            fac = __uint_as_float((uint32_t)(e - 14 + 127) << 23) * a.scale_log2;
-          }
-#pragma unroll 2
-          for (int d = 0; d < D; d += 8) {
-            float x[8];
-            if (!in) {
+    };
+    auto next_head = [&]() {
+      const uint32_t st = mcount % kMetaSlots;
+      alive = __all_sync(0xffffffffu, wait(&sh.meta_full[st], (mcount / kMetaSlots) & 1));
+      if (!alive) return make_int4(4, 0, 0, 0);
+      const int4 h = *reinterpret_cast<const int4*>(&sh.meta[st]);
+      if (!(h.x & 1)) free_entry();
+      return h;
+    };
+    int4 head4 = next_head();
+    int done_flags = 0;      // of the stretch whose results are still to be taken; 0: none
+    for (;;) {
+      const int flags = head4.x, base = head4.y;
+      const float ks = __int_as_float(head4.z), lv = __int_as_float(head4.w);
+      const bool skip = X >= flags >> 8;
+      if (rare(flags & 5)) {
+        // what the results of the last stretch need
+        const bool o_in = in;
+        const float o_l = l, o_ref = ref, o_unit = unit;
+        T* const o_out = out;
+        const int o_steps = in_stretch;
+        if ((flags & 1) && !skip) {
+          // the next stretch's queries first: its first product runs while
+          // the last one's results are taken
+          const StepMeta& m = sh.meta[mcount % kMetaSlots];
+          const int at = m.row0 + X * 128 + row;             // row of the sequence and head
+          const int tok = at / g, head = m.h * g + at % g;
+          in = X * 128 + row < m.rows;
+          pos = m.len - m.n + tok;
+          if (!in || pos < -1) pos = -1;
+          const T* q =
+              static_cast<const T*>(a.q) + (long long)(m.begin + tok) * a.q_tok + (long long)head * a.q_head;
+          out = static_cast<T*>(a.out) + (long long)(m.begin + tok) * a.o_tok + (long long)head * a.o_head;
+          // The warp reads its 32 rows together, 16 bytes a lane (a thread
+          // per row took 35000 cycles for a tile), and scales each so that
+          // its largest element is in [2^14, 2^15).
+          constexpr int E = Elem<T>::E, LPR = D / E, RPL = 32 / LPR;  // elements per lane, lanes per row, rows per load
+          const unsigned in_mask = __ballot_sync(0xffffffffu, in);
+          const bool wide_ok = __all_sync(0xffffffffu, !in || (reinterpret_cast<uintptr_t>(q) & 15) == 0);
+          const int d = lane % LPR * E;
+#pragma unroll 1
+          for (int i0 = 0; i0 < LPR; i0 += 8) {
+            uint4 raw[8];
 #pragma unroll
-              for (int i = 0; i < 8; ++i) x[i] = 0.f;
-            } else if (wide_ok) {
+            for (int i = 0; i < 8; ++i) {
+              const int r = (i0 + i) * RPL + lane / LPR;
+              const T* src = reinterpret_cast<const T*>(
+                                 __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(q), r)) + d;
+              raw[i] = make_uint4(0, 0, 0, 0);
+              if ((in_mask >> r) & 1) {
+                if (wide_ok) {
+                  raw[i] = *reinterpret_cast<const uint4*>(src);
+                } else {
+                  T* one = reinterpret_cast<T*>(&raw[i]);
 #pragma unroll
-              for (int i = 0; i < 8 / E; ++i)
-                Elem<T>::load(*reinterpret_cast<const uint4*>(q + d + i * E), x + i * E);
-            } else {
-#pragma unroll
-              for (int i = 0; i < 8; ++i) x[i] = kv_to_float<T>(q[d + i]);
-            }
-            if (!pass) {
-#pragma unroll
-              for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[i]));
-            } else {
-              uint32_t h[4], lo[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const float x0 = x[2 * i] * up, x1 = x[2 * i + 1] * up;
-                h[i] = pack_f16(x0, x1);
-                if constexpr (NP == 2) {
-                  const float2 f = f16x2_to_f32x2(h[i]);
-                  lo[i] = pack_f16(x0 - f.x, x1 - f.y);
+                  for (int e = 0; e < E; ++e) one[e] = src[e];
                 }
               }
-              const uint32_t off = (d >> 6) * 16384u + row * 128u + ((((d & 63) >> 3) ^ (row & 7)) << 4);
-              sts128(q_s + X * NP * Sh::kQ + off, h[0], h[1], h[2], h[3]);
-              if constexpr (NP == 2) sts128(q_s + (X * NP + 1) * Sh::kQ + off, lo[0], lo[1], lo[2], lo[3]);
             }
-          }
-        }
-        pos = m.len - m.n + tok;
-        if (!in || pos < -1) pos = -1;
-        ref = -INFINITY;
-        l = 0.f;
-        unit = 0.f;
-        has_unit = false;
-        fence_proxy_async_cta();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_local(smem_addr(&sh.qready[X]));
-      }
-      alive = wait(&sh.sfull[X], n_steps & 1);
-      alive = __all_sync(0xffffffffu, alive);
-      if (!alive) break;
-      tc_fence_after();
-      // keys of half h that this row sees: columns [from, to] and below `sink`
-      const float f[2] = {fac * m.ks[0], fac * m.ks[1]};
-      bool whole[2];
-      int from[2], to[2], sink[2];
-      const int low = a.window == 0 || a.window > pos ? 0 : pos - a.window + 1;
-      const int w_min = __reduce_min_sync(0xffffffffu, in ? pos : INT_MAX), w_max = __reduce_max_sync(0xffffffffu, pos);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int b = m.base[h];
-        whole[h] = b >= 0 && b + kKvPage - 1 <= w_min &&
-                   (a.window == 0 || b > w_max - a.window || b + kKvPage - 1 < a.sinks);
-        to[h] = b < 0 ? -1 : pos - b;
-        from[h] = low - b;
-        sink[h] = b < 0 ? 0 : a.sinks - b;
-      }
-      float top = -INFINITY;
+            for (int i = 0; i < 8; ++i) {
+              const int r = (i0 + i) * RPL + lane / LPR, trow = (warp & 3) * 32 + r;
+              float x[E], top = 0.f;
+              Elem<T>::load(raw[i], x);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float t = -INFINITY;
+              for (int e = 0; e < E; ++e) top = fmaxf(top, fabsf(x[e]));
 #pragma unroll
-        for (int c = 0; c < 64; c += 32) {
-          float s[32];
-          tmem_ld32(t_s + h * 64 + c, s);
-          if (whole[h]) {
+              for (int o = LPR / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+              int ex = (int)(__float_as_uint(top) >> 23) - 127;
+              ex = ex < -112 ? -112 : ex;
+              const float up = __uint_as_float((uint32_t)(14 - ex + 127) << 23);
+              if (lane % LPR == 0)
+                sh.fac[X][trow] = __uint_as_float((uint32_t)(ex - 14 + 127) << 23) * a.scale_log2;
+              uint32_t h[E / 2], lo[E / 2];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) t = fmaxf(t, s[i]);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const int k = c + i;
-              if (k <= to[h] && (k >= from[h] || k < sink[h])) t = fmaxf(t, s[i]);
-            }
-          }
-        }
-        if (t != -INFINITY) top = fmaxf(top, t * f[h]);
-        __syncwarp();
-      }
-      // raise the reference only when the weights would grow past 2^kLazy
-      float alpha = 1.f;
-      if (top > ref + kLazy || (ref == -INFINITY && top != -INFINITY)) {
-        alpha = ex2(ref - top);  // 0 from -infinity
-        ref = top;
-        l *= alpha;
-      }
-      // O's unit (the same for every row)
-      float most = -INFINITY, least = INFINITY;
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        if (m.base[h] >= 0) {
-          most = fmaxf(most, m.lv[h]);
-          least = fminf(least, m.lv[h]);
-        }
-      if (most != -INFINITY && (!has_unit || most - unit > kUnit || unit - least > kUnit)) {
-        if (has_unit) alpha *= ex2(unit - most);
-        unit = most;
-        has_unit = true;
-      }
-      if (!(m.flags & 1) && __any_sync(0xffffffffu, alpha != 1.f)) {
-#pragma unroll 1
-        for (int c = 0; c < D; c += 16) {
-          float o[16];
-          tmem_ld16(t_o + c, o);
-          uint32_t r[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(o[i] * alpha);
-          tmem_st16(t_o + c, r);
-        }
-      }
-      const float zero = ref == -INFINITY ? 0.f : ref;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float shift = m.base[h] >= 0 ? m.lv[h] - unit : 0.f;
-        const float add = shift - zero + kLift;
-        float sum = 0.f;
-#pragma unroll
-        for (int c = 0; c < 64; c += 32) {
-          float s[32];
-          tmem_ld32(t_s + h * 64 + c, s);
-          if (whole[h]) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) s[i] = ex2(fmaf(s[i], f[h], add));
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const int k = c + i;
-              const bool see = k <= to[h] && (k >= from[h] || k < sink[h]);
-              s[i] = see ? ex2(fmaf(s[i], f[h], add)) : 0.f;
-            }
-          }
-          uint32_t r[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            sum += s[2 * i] + s[2 * i + 1];
-            r[i] = pack_f16(s[2 * i], s[2 * i + 1]);
-          }
-          tmem_st16(t_p + h * 32 + c / 2, r);
-          if constexpr (NP == 2) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float2 b = f16x2_to_f32x2(r[i]);
-              r[i] = pack_f16(s[2 * i] - b.x, s[2 * i + 1] - b.y);
-            }
-            tmem_st16(t_p + 64 + h * 32 + c / 2, r);
-          }
-        }
-        l = fmaf(sum, ex2(-shift), l);
-      }
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_local(smem_addr(&sh.pready[X]));
-      ++n_steps;
-
-      if (m.flags & 2) {
-        alive = wait(&sh.pvdone[X], (n_steps - 1) & 1);
-        alive = __all_sync(0xffffffffu, alive);
-        if (!alive) break;
-        tc_fence_after();
-        const bool cut = (m.flags & 24) != 24;
-        const int slot = 2 * blockIdx.x + ((m.flags & 8) ? 1 : 0);
-        float* po = TilePartial<D, R>::o(a.ws, slot) + (size_t)(X * 128 + row) * D;
-        T* out = static_cast<T*>(a.out) + (long long)(m.begin + tok) * a.o_tok + (long long)head * a.o_head;
-        const bool wide_ok = (reinterpret_cast<uintptr_t>(out) & 15) == 0;
-        const float back = ex2(unit);  // O in the values' own unit
-        const float inv = l == 0.f ? 0.f : back / l;
-        if (cut && in) {
-          TilePartial<D, R>::m(a.ws, slot)[X * 128 + row] = ref;
-          TilePartial<D, R>::l(a.ws, slot)[X * 128 + row] = l;
-        }
-        __syncwarp();
-#pragma unroll 1
-        for (int c = 0; c < D; c += 16) {
-          float o[16];
-          tmem_ld16(t_o + c, o);
-          if (in) {
-            if (cut) {
-#pragma unroll
-              for (int i = 0; i < 16; i += 4)
-                *reinterpret_cast<float4*>(po + c + i) = make_float4(o[i] * back, o[i + 1] * back, o[i + 2] * back, o[i + 3] * back);
-            } else {
-#pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] *= inv;
-              if (wide_ok) {
-#pragma unroll
-                for (int i = 0; i < 16; i += Elem<T>::E)
-                  *reinterpret_cast<uint4*>(out + c + i) = pack_chunk<T>(o + i);
+              for (int e = 0; e < E / 2; ++e) {
+                const float x0 = x[2 * e] * up, x1 = x[2 * e + 1] * up;
+                h[e] = pack_f16(x0, x1);
+                const float2 f = f16x2_to_f32x2(h[e]);
+                lo[e] = pack_f16(x0 - f.x, x1 - f.y);
+              }
+              const uint32_t off = X * NP * Sh::kQ + (d >> 6) * 16384u + trow * 128u +
+                                   ((((d & 63) >> 3) ^ (trow & 7)) << 4);
+              if constexpr (NP == 1) {
+                sts128(q_s + off, h[0], h[1], h[2], h[3]);
               } else {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) out[c + i] = kv_from_float<T>(o[i]);
+                sts64(q_s + off + (d & 4) * 2, h[0], h[1]);
+                sts64(q_s + off + Sh::kQ + (d & 4) * 2, lo[0], lo[1]);
               }
             }
           }
           __syncwarp();
+          fac = sh.fac[X][(warp & 3) * 32 + lane];
+          ref = -INFINITY;
+          l = 0.f;
+          unit = NAN;
+          w_min = __reduce_min_sync(0xffffffffu, in ? pos : INT_MAX);
+          w_max = __reduce_max_sync(0xffffffffu, pos);
+          fence_proxy_async_cta();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_local(smem_addr(&sh.qready[X]));
         }
-        tc_fence_before();  // before the next stretch's products overwrite O
+        if (flags & 1) free_entry();
+        if (done_flags) {
+          wait(&sh.pvdone[X], (n_steps - 1) & 1);
+          __syncwarp();
+          tc_fence_after();
+          const bool cut = (done_flags & 24) != 24;
+          const int slot = 2 * blockIdx.x + ((done_flags & 8) ? 1 : 0);
+          float* po = TilePartial<D, R>::o(a.ws, slot) + (size_t)(X * 128 + row) * D;
+          const bool wide_ok = (reinterpret_cast<uintptr_t>(o_out) & 15) == 0;
+          const float back = o_unit == o_unit ? ex2(o_unit) : 1.f;  // O in the values' own unit
+          const float mul = cut ? back : o_l == 0.f ? 0.f : back / o_l;
+          if (cut && o_in) {
+            TilePartial<D, R>::m(a.ws, slot)[X * 128 + row] = o_ref;
+            TilePartial<D, R>::l(a.ws, slot)[X * 128 + row] = o_l;
+          }
+          __syncwarp();
+#pragma unroll 1
+          for (int c = 0; c < D; c += 64) {
+            float o[64];
+            tmem_ld64(t_o + c, o);
+            tmem_landed64(o);
+            if constexpr (NP == 2) {
+              if (o_steps >= kFold) {
+#pragma unroll
+                for (int k = 0; k < 64; k += 16) {
+                  float acc[16];
+                  tmem_ld16(t_acc + c + k, acc);
+#pragma unroll
+                  for (int i = 0; i < 16; ++i) o[k + i] += acc[i];
+                }
+              }
+            }
+            if (o_in) {
+#pragma unroll
+              for (int i = 0; i < 64; ++i) o[i] *= mul;
+              if (cut) {
+#pragma unroll
+                for (int i = 0; i < 64; i += 4)
+                  *reinterpret_cast<float4*>(po + c + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+              } else if (wide_ok) {
+#pragma unroll
+                for (int i = 0; i < 64; i += Elem<T>::E)
+                  *reinterpret_cast<uint4*>(o_out + c + i) = pack_chunk<T>(o + i);
+              } else {
+#pragma unroll
+                for (int i = 0; i < 64; ++i) o_out[c + i] = kv_from_float<T>(o[i]);
+              }
+            }
+            __syncwarp();
+          }
+          tc_fence_before();  // before the next stretch's products overwrite O
+          done_flags = 0;
+        }
+        if (flags & 4) break;
       }
+      if (skip) {
+        head4 = next_head();
+        continue;
+      }
+      in_stretch = flags & 1 ? 0 : in_stretch + 1;
+      const uint32_t buf = n_steps & 1;
+      const uint32_t t_s = lanes + Sh::S(X) + buf * 64;
+      // (a wait that gives up is seen at the next entry; what is computed
+      // until then goes nowhere)
+      kv_wait2(&sh.sfull[X][buf], (n_steps >> 1) & 1, &sh.meta_full[mcount % kMetaSlots], (mcount / kMetaSlots) & 1,
+               abort, a.kv.err);
+      __syncwarp();
+      tc_fence_after();
+      float v[64];
+      tmem_ld64(t_s, v);
+      head4 = next_head();
+      tmem_landed64(v);
+      // a page that some row of the warp does not see all of: its hidden
+      // places become -infinity
+      const bool whole = base >= 0 && base + kKvPage - 1 <= w_min &&
+                         (a.window == 0 || base > w_max - a.window || base + kKvPage - 1 < a.sinks);
+      if (rare(!whole)) {
+        const int low = a.window == 0 || a.window > pos ? 0 : pos - a.window + 1;
+        const int to = base < 0 ? -1 : pos - base, from = low - base, sink = base < 0 ? 0 : a.sinks - base;
+#pragma unroll
+        for (int k = 0; k < 64; ++k) v[k] = k <= to && (k >= from || k < sink) ? v[k] : -INFINITY;
+      }
+      // Key scales are positive; a page whose factor is 0 (an empty query) is
+      // kept off 0 * -infinity by the floor, which moves no visible weight.
+      const float f = fmaxf(fac * ks, 1.17549435e-38f);
+      float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int k = 0; k < 64; k += 8)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) t[i] = fmaxf(fmaxf(t[i], v[k + 2 * i]), v[k + 2 * i + 1]);
+      const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * f;
+      // Seldom: a row's maximum has grown past what its weights may show, the
+      // page's value scale is too far from O's unit (the same for all rows),
+      // or it is time for a fold.
+      const bool raise = top > ref + kLazy;
+      const bool fold = NP == 2 && in_stretch && in_stretch % kFold == 0;
+      const bool switch_unit = base >= 0 && !(fabsf(lv - unit) <= kUnit);
+      if (rare(__any_sync(0xffffffffu, raise || fold || switch_unit))) {
+        float alpha = 1.f;
+        if (raise) {
+          alpha = ex2(ref - top);  // 0 from -infinity
+          ref = top;
+          l *= alpha;
+        }
+        if (switch_unit) {
+          if (unit == unit) alpha *= ex2(unit - lv);
+          unit = lv;
+        }
+        if (in_stretch) {
+          // O rests once the last P V is done
+          wait(&sh.pvdone[X], (n_steps - 1) & 1);
+          __syncwarp();
+          tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < D; c += 16) {
+          float o[16];
+          uint32_t r[16];
+          tmem_ld16(t_o + c, o);
+          if constexpr (NP == 2) {
+            // O and the second accumulator: scaled, and added up at a fold
+            if (in_stretch >= kFold) {
+              float acc[16];
+              if (in_stretch > kFold) {
+                tmem_ld16(t_acc + c, acc);
+              } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) acc[i] = 0.f;
+              }
+#pragma unroll
+              for (int i = 0; i < 16; ++i) r[i] = __float_as_uint((fold ? acc[i] + o[i] : acc[i]) * alpha);
+              tmem_st16(t_acc + c, r);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(o[i] * alpha);
+          tmem_st16(t_o + c, r);
+        }
+        }
+      }
+      const float shift = base >= 0 ? lv - unit : 0.f;
+      const float add1 = shift - (ref == -INFINITY ? 0.f : ref) + kLift;
+      const float2 mul = make_float2(f, f), add = make_float2(add1, add1);
+      float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+      for (int c = 0; c < 64; c += 32) {
+        uint32_t r[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          float* x = v + c + 2 * i;
+          float2 e = fma2(make_float2(x[0], x[1]), mul, add);
+          e.x = ex2(e.x);
+          e.y = ex2(e.y);
+          sum[i & 1] = add2(sum[i & 1], e);
+          r[i] = pack_f16(e.x, e.y);
+          if constexpr (NP == 2) {
+            x[0] = e.x;
+            x[1] = e.y;
+          }
+        }
+        tmem_st16(t_s + c / 2, r);
+        if constexpr (NP == 2) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float* x = v + c + 2 * i;
+            const float2 b = f16x2_to_f32x2(r[i]);
+            r[i] = pack_f16(x[0] - b.x, x[1] - b.y);
+          }
+          tmem_st16(t_s + 32 + c / 2, r);
+        }
+      }
+      tmem_wait_st();
+      if (rare((flags & 2) && in_stretch)) {
+        // The wait for this step's P V below can tell it from the one before
+        // by parity only once that one is done; here it cannot have begun.
+        wait(&sh.pvdone[X], (n_steps - 1) & 1);
+        __syncwarp();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_local(smem_addr(&sh.pready[X][buf]));
+      const float2 both = add2(sum[0], sum[1]);
+      l = fmaf(both.x + both.y, ex2(-shift), l);
+      ++n_steps;
+
+      if (flags & 2) done_flags = flags;
+    }
     }
   }
   __syncwarp();
@@ -953,7 +1093,7 @@ __global__ void __launch_bounds__(256) tile_join_kernel(const KvAttend a, int ct
   const TileKeys tk = tile_keys<R>(a, w.n, w.len, t.tile);
   const int row = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (row >= tk.rows) return;
-  const int more = (int)((tk.steps() - t.step + p.chunk - 1) / p.chunk);
+  const int more = (int)((tk.pages - t.step + p.chunk - 1) / p.chunk);
   const int c0 = blockIdx.x - 1;
   float top = TilePartial<D, R>::m(a.ws, 2 * c0 + 1)[row];
   for (int i = 1; i <= more; ++i) top = fmaxf(top, TilePartial<D, R>::m(a.ws, 2 * (c0 + i))[row]);
