@@ -68,6 +68,20 @@ __device__ __forceinline__ KvSeq kv_seq(const KvView& kv, const KvBatch& b, int 
   return s;
 }
 
+// An item of attention work that is cut between CTAs: CTA c leaves this at the
+// head of the workspace about the cut in front of its share, for the launch
+// that joins the partials.
+struct __align__(16) KvCut {
+  int more;   // partials after the first, from this CTA on; 0: no item is joined from here
+  int row0;   // first row of the item in its sequence and head (a row: new token x query head)
+  int rows;
+  int begin;  // first new token of the sequence
+  int h;      // key/value head
+  int pad[3];
+};
+constexpr int kKvMaxCtas = 256;  // upper bound of an attention grid
+constexpr size_t kKvCutBytes = kKvMaxCtas * sizeof(KvCut);
+
 // Attention of one layer (np_kv_attend).
 struct KvAttend {
   KvView kv;

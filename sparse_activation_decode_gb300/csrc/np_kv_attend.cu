@@ -48,7 +48,6 @@ namespace np {
 
 namespace {
 
-constexpr int kMaxCtas = 256;       // upper bound of the grid (workspace)
 constexpr int kMaxAttendStages = 16;
 constexpr int kTileRows = 16;       // sequences with more rows go to the tiled kernel
 constexpr int kWholePages = 8;      // items of at most this many pages are never cut
@@ -306,7 +305,9 @@ __device__ __forceinline__ bool wait_page(volatile StageMeta* meta, uint64_t* ba
 // item, 2c + 1 for one that begins an item it does not end.
 template <int D, int R> struct Partial {
   static constexpr size_t kFloats = (size_t)R * (D + 2);
-  __device__ static float* o(void* ws, int slot) { return static_cast<float*>(ws) + slot * kFloats; }
+  __device__ static float* o(void* ws, int slot) {
+    return reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kKvCutBytes) + slot * kFloats;
+  }
   __device__ static float* m(void* ws, int slot) { return o(ws, slot) + R * D; }
   __device__ static float* l(void* ws, int slot) { return o(ws, slot) + R * D + R; }
 };
@@ -357,6 +358,21 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
     const uint64_t once = policy_evict_first();
     uint32_t count = 0;  // pages handed out
     bool alive = true;
+    if (lane == 0) {
+      KvCut cut{};
+      if (p.split && u0 < u1) {
+        const Segment s = segment_at<R>(a, p, pre, seq, u0, p.total);
+        if (!s.starts && s.k0 <= p.chunk) {  // the first cut inside this item
+          cut.more = (int)((s.pages.count - s.k0 + p.chunk - 1) / p.chunk);
+          cut.row0 = s.tile * R;
+          cut.rows = tile_rows<R>(a, seq[s.b], s.tile).rows;
+          cut.begin = seq[s.b].begin;
+          cut.h = s.h;
+        }
+      }
+      static_cast<KvCut*>(a.ws)[blockIdx.x] = cut;
+    }
+    __syncwarp();
     for (long long u = u0; u < u1 && alive;) {
       const Segment s = segment_at<R>(a, p, pre, seq, u, u1);
       const SeqWork w = seq[s.b];
@@ -702,44 +718,32 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
   }
 }
 
-// Joins the partials of items that were cut.  CTA c looks at the cut between
-// the shares c - 1 and c; the first cut inside an item does the item.
+// Joins the partials of an item that was cut: CTA (c, y) elements 32 y .. of
+// the item that the cut in front of share c opens, a thread per row and element.
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(256) attend_join_kernel(const KvAttend a, int ctas) {
+__global__ void __launch_bounds__(256) attend_join_kernel(const KvAttend a) {
   constexpr int R = 8 * NT;
-  extern __shared__ __align__(1024) uint8_t smem_raw[];
-  __shared__ long long tmp[2];
-  long long* pre = reinterpret_cast<long long*>(smem_raw);
-  SeqWork* seq = reinterpret_cast<SeqWork*>(pre + a.batch.n_seqs + 1 + ((a.batch.n_seqs + 1) & 1));
-  const Plan p = plan<R>(a, ctas, pre, seq, tmp);
   grid_dependency_wait();
-  const long long u = (long long)blockIdx.x * p.chunk;
-  if (!p.split || u >= p.total) return;
-  const Segment s = segment_at<R>(a, p, pre, seq, u, p.total);
-  if (s.starts) return;                   // the cut falls between two items
-  if (s.k0 > p.chunk) return;             // the previous cut lies inside the same item
-  const SeqWork w = seq[s.b];
-  const TileRows t = tile_rows<R>(a, w, s.tile);
-  const int g = a.Hq / a.kv.H;
-  const int more = (int)((s.pages.count - s.k0 + p.chunk - 1) / p.chunk);  // partials after the first
-  const int c0 = blockIdx.x - 1;
-  for (int x = threadIdx.x; x < t.rows * 32; x += 256) {
+  const KvCut cut = static_cast<const KvCut*>(a.ws)[blockIdx.x];
+  if (cut.more == 0) return;
+  const int c0 = blockIdx.x - 1, g = a.Hq / a.kv.H;
+  for (int x = threadIdx.x; x < cut.rows * 32; x += 256) {
     const int row = x / 32, d = blockIdx.y * 32 + x % 32;
     float top = Partial<D, R>::m(a.ws, 2 * c0 + 1)[row];
-#pragma unroll 4
-    for (int i = 1; i <= more; ++i) top = fmaxf(top, Partial<D, R>::m(a.ws, 2 * (c0 + i))[row]);
+#pragma unroll 8
+    for (int i = 1; i <= cut.more; ++i) top = fmaxf(top, Partial<D, R>::m(a.ws, 2 * (c0 + i))[row]);
     const float ref = top == -INFINITY ? 0.f : top;
     float sum = 0.f, y = 0.f;
-#pragma unroll 4
-    for (int i = 0; i <= more; ++i) {
+#pragma unroll 8
+    for (int i = 0; i <= cut.more; ++i) {
       const int slot = 2 * (c0 + i) + (i == 0 ? 1 : 0);
       const float f = ex2(Partial<D, R>::m(a.ws, slot)[row] - ref);
       sum = fmaf(Partial<D, R>::l(a.ws, slot)[row], f, sum);
       y = fmaf(Partial<D, R>::o(a.ws, slot)[row * D + d], f, y);
     }
-    const int at = s.tile * R + row;
-    T* out = static_cast<T*>(a.out) + (long long)(w.begin + at / g) * a.o_tok +
-             (long long)(s.h * g + at % g) * a.o_head + d;
+    const int at = cut.row0 + row;
+    T* out = static_cast<T*>(a.out) + (long long)(cut.begin + at / g) * a.o_tok +
+             (long long)(cut.h * g + at % g) * a.o_head + d;
     *out = kv_from_float<T>(sum == 0.f ? 0.f : y / sum);
   }
 }
@@ -776,8 +780,8 @@ cudaError_t launch_stream(const KvAttend& a, cudaStream_t st) {
     if (seen < most) most = seen;
   }
   if (most <= kWholePages) return cudaSuccess;
-  PdlConfig pdl(dim3((unsigned)ctas, D / 32), dim3(256), list, st);
-  return cudaLaunchKernelEx(&pdl.cfg, attend_join_kernel<T, D, NT>, a, ctas);
+  PdlConfig pdl(dim3((unsigned)ctas, D / 32), dim3(256), 0, st);
+  return cudaLaunchKernelEx(&pdl.cfg, attend_join_kernel<T, D, NT>, a);
 }
 
 template <typename T>
@@ -797,7 +801,7 @@ int kv_attend_ctas() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
   if (n[dev] == 0) cudaDeviceGetAttribute(&n[dev], cudaDevAttrMultiProcessorCount, dev);
-  return n[dev] < kMaxCtas ? n[dev] : kMaxCtas;
+  return n[dev] < kKvMaxCtas ? n[dev] : kKvMaxCtas;
 }
 
 static bool takes_tile(int dtype, int head_dim, long long rows) {
@@ -805,7 +809,7 @@ static bool takes_tile(int dtype, int head_dim, long long rows) {
 }
 
 size_t kv_attend_workspace(int dtype, int head_dim, long long rows) {
-  const size_t stream = (size_t)2 * kMaxCtas * (head_dim == 256 ? 8 : 16) * (head_dim + 2) * sizeof(float);
+  const size_t stream = kKvCutBytes + (size_t)2 * kKvMaxCtas * (head_dim == 256 ? 8 : 16) * (head_dim + 2) * sizeof(float);
   const size_t tile = takes_tile(dtype, head_dim, rows) ? kv_tile_workspace(dtype, head_dim) : 0;
   return stream > tile ? stream : tile;
 }

@@ -12,10 +12,10 @@
 // goes into the weights, w = 2^(s - M + lv - LV) with lv = log2(v_scale) and
 // LV the unit that O is held in, so O needs no scaling per page; the softmax
 // sum takes w 2^(LV - lv).  When a page's lv is more than 3 away from LV, O
-// is multiplied (fp32) into the unit of that page: a weight that fp16 cannot
-// hold is below 2^-29 of its row's largest, whatever the scales.  M is raised
-// only when a row's maximum has grown by more than 2^4 since it was set, so
-// that O is seldom rescaled; weights carry a factor 2^8.  For fp32 outputs O
+// is multiplied (fp32) into the unit of that page: a weight that fp16 rounds to
+// less than 11 bits is below 2^-17 of its row's largest, whatever the scales.  M is raised
+// only when a row's maximum has grown by more than 2^6 since it was set, so
+// that O is seldom rescaled; weights carry a factor 2^6.  For fp32 outputs O
 // is added to a second accumulator every 8 steps: the tensor core's own adds
 // truncate, and over n of them their bias is n 2^-25.
 //
@@ -55,7 +55,7 @@ constexpr int kFold = 8;  // steps between additions into the second accumulator
 // log2 of: the growth a weight may show before M is raised, the distance of a
 // page's value scale from O's unit, the factor on all weights.  Together they
 // stay below fp16's largest, 2^16.
-constexpr float kLazy = 4.f, kUnit = 3.f, kLift = 8.f;
+constexpr float kLazy = 6.f, kUnit = 3.f, kLift = 6.f;
 constexpr int kCutCost = 16;   // steps that cutting an item costs (partials, second launch)
 
 // NX tiles of 128 rows, NP fp16 parts of Q and P, NB operand buffers.
@@ -387,6 +387,11 @@ __device__ __forceinline__ void widen16(const uint4& v, uint32_t a0, uint32_t a1
 // Codes that are NaN become 0.
 __device__ __forceinline__ uint32_t clean4(uint32_t w) { return w & ~__vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu); }
 
+// Bits 0 .. n - 1 of 64.
+__device__ __forceinline__ uint64_t bits_below(long long n) {
+  return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1;
+}
+
 // Code that few steps run goes out of the loops' way: the roles' loops together
 // have to stay in the instruction cache.
 __device__ __forceinline__ bool rare(bool c) { return __builtin_expect(c, 0); }
@@ -404,7 +409,9 @@ struct TileShared {
 
 template <int D, int R> struct TilePartial {
   static constexpr size_t kFloats = (size_t)R * (D + 2);
-  __device__ static float* o(void* ws, int slot) { return static_cast<float*>(ws) + slot * kFloats; }
+  __device__ static float* o(void* ws, int slot) {
+    return reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kKvCutBytes) + slot * kFloats;
+  }
   __device__ static float* m(void* ws, int slot) { return o(ws, slot) + R * D; }
   __device__ static float* l(void* ws, int slot) { return o(ws, slot) + R * D + R; }
 };
@@ -476,8 +483,17 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const KvAt
       alive = __all_sync(0xffffffffu, alive);
       return alive;
     };
+    KvCut cut{};
     if (u0 < u1) {
       TilePos t = tile_find<R>(a, p, pre, per, seq, u0);
+      if (t.step > 0 && t.step <= p.chunk) {  // the first cut inside this item
+        const TileKeys tk = tile_keys<R>(a, seq[t.b].n, seq[t.b].len, t.tile);
+        cut.more = (int)((tk.pages - t.step + p.chunk - 1) / p.chunk);
+        cut.row0 = t.tile * R;
+        cut.rows = tk.rows;
+        cut.begin = seq[t.b].begin;
+        cut.h = t.h;
+      }
       for (long long u = u0; u < u1 && alive;) {
         const TileSeq w = seq[t.b];
         const TileKeys tk = tile_keys<R>(a, w.n, w.len, t.tile);
@@ -548,6 +564,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const KvAt
         }
       }
     }
+    if (lane == 0) static_cast<KvCut*>(a.ws)[blockIdx.x] = cut;
     if (slot_free()) {
       if (lane == 0) {
         sh.meta[count % kMetaSlots].flags = 4;
@@ -954,8 +971,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const KvAt
       if (rare(!whole)) {
         const int low = a.window == 0 || a.window > pos ? 0 : pos - a.window + 1;
         const int to = base < 0 ? -1 : pos - base, from = low - base, sink = base < 0 ? 0 : a.sinks - base;
+        const uint64_t see = bits_below((long long)to + 1) & (~bits_below(from) | bits_below(sink));
+        const uint32_t see0 = (uint32_t)see, see1 = (uint32_t)(see >> 32);
 #pragma unroll
-        for (int k = 0; k < 64; ++k) v[k] = k <= to && (k >= from || k < sink) ? v[k] : -INFINITY;
+        for (int k = 0; k < 32; ++k) {
+          v[k] = see0 & (1u << k) ? v[k] : -INFINITY;
+          v[k + 32] = see1 & (1u << k) ? v[k + 32] : -INFINITY;
+        }
       }
       // Key scales are positive; a page whose factor is 0 (an empty query) is
       // kept off 0 * -infinity by the floor, which moves no visible weight.
@@ -1072,48 +1094,40 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const KvAt
   }
 }
 
-// Joins the partials of items that were cut: CTA (c, y) rows 8 y .. 8 y + 7
-// of the item that the cut in front of share c opens.
+// Joins the partials of an item that was cut: CTA (c, y) rows 32 y .. 32 y + 31
+// of the item that the cut in front of share c opens, a warp per row.
 template <typename T, int D>
-__global__ void __launch_bounds__(256) tile_join_kernel(const KvAttend a, int ctas) {
+__global__ void __launch_bounds__(256) tile_join_kernel(const KvAttend a) {
   constexpr int R = TileShape<T, D>::R;
   constexpr int V = D / 32;  // elements per lane
-  extern __shared__ __align__(1024) uint8_t smem_raw[];
-  __shared__ long long tmp[3];
-  long long* pre = reinterpret_cast<long long*>(smem_raw);
-  TileSeq* seq = reinterpret_cast<TileSeq*>(pre + a.batch.n_seqs + 1 + ((a.batch.n_seqs + 1) & 1));
-  int* per = reinterpret_cast<int*>(seq + a.batch.n_seqs);
-  const TilePlan p = tile_plan<R>(a, ctas, pre, per, seq, tmp);
   grid_dependency_wait();
-  const long long u = (long long)blockIdx.x * p.chunk;
-  if (!p.split || u >= p.total) return;
-  const TilePos t = tile_find<R>(a, p, pre, per, seq, u);
-  if (t.step == 0 || t.step > p.chunk) return;  // the cut lies between items, or not first in its item
-  const TileSeq w = seq[t.b];
-  const TileKeys tk = tile_keys<R>(a, w.n, w.len, t.tile);
-  const int row = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (row >= tk.rows) return;
-  const int more = (int)((tk.pages - t.step + p.chunk - 1) / p.chunk);
-  const int c0 = blockIdx.x - 1;
-  float top = TilePartial<D, R>::m(a.ws, 2 * c0 + 1)[row];
-  for (int i = 1; i <= more; ++i) top = fmaxf(top, TilePartial<D, R>::m(a.ws, 2 * (c0 + i))[row]);
-  const float zero = top == -INFINITY ? 0.f : top;
-  float sum = 0.f, y[V];
+  const KvCut cut = static_cast<const KvCut*>(a.ws)[blockIdx.x];
+  if (cut.more == 0) return;
+  const int lane = threadIdx.x & 31, c0 = blockIdx.x - 1, g = a.Hq / a.kv.H;
+  for (int i = 0; i < 4; ++i) {
+    const int row = blockIdx.y * 32 + i * 8 + (threadIdx.x >> 5);
+    if (row >= cut.rows) continue;
+    float top = TilePartial<D, R>::m(a.ws, 2 * c0 + 1)[row];
+    for (int k = 1; k <= cut.more; ++k) top = fmaxf(top, TilePartial<D, R>::m(a.ws, 2 * (c0 + k))[row]);
+    const float zero = top == -INFINITY ? 0.f : top;
+    float sum = 0.f, y[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) y[i] = 0.f;
-  for (int i = 0; i <= more; ++i) {
-    const int slot = 2 * (c0 + i) + (i == 0 ? 1 : 0);
-    const float f = ex2(TilePartial<D, R>::m(a.ws, slot)[row] - zero);
-    sum = fmaf(TilePartial<D, R>::l(a.ws, slot)[row], f, sum);
-    const float* o = TilePartial<D, R>::o(a.ws, slot) + (size_t)row * D + lane;
+    for (int j = 0; j < V; ++j) y[j] = 0.f;
+    for (int k = 0; k <= cut.more; ++k) {
+      const int slot = 2 * (c0 + k) + (k == 0 ? 1 : 0);
+      const float f = ex2(TilePartial<D, R>::m(a.ws, slot)[row] - zero);
+      sum = fmaf(TilePartial<D, R>::l(a.ws, slot)[row], f, sum);
+      const float* o = TilePartial<D, R>::o(a.ws, slot) + (size_t)row * D + lane;
 #pragma unroll
-    for (int j = 0; j < V; ++j) y[j] = fmaf(o[32 * j], f, y[j]);
+      for (int j = 0; j < V; ++j) y[j] = fmaf(o[32 * j], f, y[j]);
+    }
+    const int at = cut.row0 + row;
+    T* out = static_cast<T*>(a.out) + (long long)(cut.begin + at / g) * a.o_tok +
+             (long long)(cut.h * g + at % g) * a.o_head;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+    for (int j = 0; j < V; ++j) out[lane + 32 * j] = kv_from_float<T>(y[j] * inv);
   }
-  const int g = a.Hq / a.kv.H, at = t.tile * R + row;
-  T* out = static_cast<T*>(a.out) + (long long)(w.begin + at / g) * a.o_tok + (long long)(t.h * g + at % g) * a.o_head;
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-  for (int j = 0; j < V; ++j) out[lane + 32 * j] = kv_from_float<T>(y[j] * inv);
 }
 
 template <typename T, int D> struct TileTag {};
@@ -1131,8 +1145,8 @@ cudaError_t launch_tile(const KvAttend& a, cudaStream_t st) {
   kern<<<ctas, kTileThreads, smem, st>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  PdlConfig pdl(dim3((unsigned)ctas, Sh::R / 8), dim3(256), list, st);
-  return cudaLaunchKernelEx(&pdl.cfg, tile_join_kernel<T, D>, a, ctas);
+  PdlConfig pdl(dim3((unsigned)ctas, Sh::R / 32), dim3(256), 0, st);
+  return cudaLaunchKernelEx(&pdl.cfg, tile_join_kernel<T, D>, a);
 }
 
 }  // namespace
@@ -1141,7 +1155,7 @@ bool kv_tile_takes(int dtype, int head_dim) { return dtype != 0 || head_dim != 2
 
 size_t kv_tile_workspace(int dtype, int head_dim) {
   const int rows = dtype == 0 || head_dim == 256 ? 128 : 256;
-  return (size_t)2 * kv_attend_ctas() * rows * (head_dim + 2) * sizeof(float);
+  return kKvCutBytes + (size_t)2 * kv_attend_ctas() * rows * (head_dim + 2) * sizeof(float);
 }
 
 cudaError_t launch_kv_tile(const KvAttend& a, cudaStream_t st) {
