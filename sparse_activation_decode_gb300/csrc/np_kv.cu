@@ -378,8 +378,9 @@ __device__ __forceinline__ float pow2f(int e) { return __uint_as_float((uint32_t
 
 // Rescale the codes of a word by a power of two.
 __device__ __forceinline__ uint32_t rescale4(uint32_t w, float r) {
-  const float2 a = f16x2_to_f32x2(e4m3x2_to_f16x2(w & 0xffffu));
-  const float2 b = f16x2_to_f32x2(e4m3x2_to_f16x2(w >> 16));
+  uint32_t lo, hi;
+  e4m3x4_to_f16x4(w, lo, hi);
+  const float2 a = f16x2_to_f32x2(lo), b = f16x2_to_f32x2(hi);
   return f32x2_to_e4m3x2(a.x * r, a.y * r) | (f32x2_to_e4m3x2(b.x * r, b.y * r) << 16);
 }
 

@@ -159,11 +159,13 @@ template <> __device__ __forceinline__ __nv_bfloat16 kv_from_float<__nv_bfloat16
   return __float2bfloat16_rn(v);
 }
 
-// Two e4m3 codes (low byte first) as two fp16 values: exact, NaN kept.
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 lo;\n\tcvt.u16.u32 lo, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(two));
-  return r;
+// Four e4m3 codes (a word, low byte first) as two words of fp16 pairs: exact,
+// NaN kept.
+__device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
 }
 
 // Two floats as two e4m3 codes (lo in the low byte), nearest, saturating.

@@ -29,7 +29,7 @@
 // contiguous shares, one CTA per SM (ragged lengths balance by construction).
 // In a CTA a producer warp streams pages through a shared-memory ring (TMA,
 // 128-byte swizzle for K so that the 16-byte reads meet no bank twice) and
-// eight warps each take every eighth page, with statistics of their own that
+// seven warps each take every seventh page, with statistics of their own that
 // are joined once per share.  A row whose pages are cut between CTAs leaves
 // fp32 partials, which a second launch joins in a fixed order.  Short items
 // are not cut (see plan()).
@@ -53,7 +53,7 @@ constexpr int kTileRows = 16;       // sequences with more rows go to the tiled 
 constexpr int kWholePages = 8;      // items of at most this many pages are never cut
 
 template <int D> struct Shape {
-  static constexpr int kWarps = D == 256 ? 4 : 8;           // consumer warps
+  static constexpr int kWarps = D == 256 ? 4 : 7;           // consumer warps: few, with many registers each
   static constexpr int kThreads = 32 * (kWarps + 1);
   static constexpr int kStage = 2 * kKvPage * D;            // bytes of one page, K then V
   static constexpr int kRowPad = D + 4;                     // floats per row of the join buffer
@@ -256,6 +256,11 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   return v;
 }
 
+// Word q of a 16-byte chunk (q a constant).
+__device__ __forceinline__ uint32_t word(const uint4& v, int q) {
+  return q == 0 ? v.x : q == 1 ? v.y : q == 2 ? v.z : v.w;
+}
+
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar,
                                             uint64_t policy) {
   asm volatile(
@@ -356,7 +361,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
   if (warp == W) {
     // ---- producer ----
     const uint64_t once = policy_evict_first();
-    uint32_t count = 0;  // pages handed out
+    uint32_t count = 0, last = 0;  // pages dealt with; one past the last that this lane has issued
     bool alive = true;
     if (lane == 0) {
       KvCut cut{};
@@ -396,40 +401,56 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             }
           }
         }
+        // each lane sees to its own page, as many at a time as the ring has
+        // stages (one page after another took 650 cycles a page, more than
+        // HBM needs for it)
         const int here = s.k1 - k0 < 32 ? s.k1 - k0 : 32;
-        for (int i = 0; i < here; ++i) {
-          const int pg = __shfl_sync(0xffffffffu, page, i), bs = __shfl_sync(0xffffffffu, base, i);
-          const float ksi = __shfl_sync(0xffffffffu, ks, i), vsi = __shfl_sync(0xffffffffu, vs, i);
-          const uint32_t st = count % ns;
-          if (count >= ns) alive = kv_wait(&empty[st], (count / ns - 1) & 1, &abort_s, a.kv.err);
-          alive = __shfl_sync(0xffffffffu, (int)alive, 0) != 0;
-          if (!alive) break;
-          if (lane == 0) {
-            meta[st].base = pg < 0 ? -1 : bs;
-            meta[st].k_scale = ksi;
-            meta[st].v_scale = vsi;
-            *reinterpret_cast<volatile uint32_t*>(&meta[st].seq) = count + 1;
-            if (pg < 0) {
-              mbar_arrive_local(smem_addr(&full[st]));
-            } else {
-              const int block = pg * a.kv.H + s.h;
-              uint8_t* dst = ring + (size_t)st * Sh::kStage;
-              mbar_arrive_expect_tx(&full[st], Sh::kStage);
+        const uint32_t i = count + lane, st = i % ns, turn = i / ns;
+        for (int b = 0; b < here && alive; b += n_stages) {
+          bool done = lane < b || lane >= b + n_stages || lane >= here;
+          uint64_t t0 = 0;
+          for (uint32_t it = 1;; ++it) {
+            if (!done && (turn == 0 || kv_test(&empty[st], (turn - 1) & 1))) {
+              meta[st].base = page < 0 ? -1 : base;
+              meta[st].k_scale = ks;
+              meta[st].v_scale = vs;
+              *reinterpret_cast<volatile uint32_t*>(&meta[st].seq) = i + 1;
+              if (page < 0) {
+                mbar_arrive_local(smem_addr(&full[st]));
+              } else {
+                const int block = page * a.kv.H + s.h;
+                uint8_t* dst = ring + (size_t)st * Sh::kStage;
+                mbar_arrive_expect_tx(&full[st], Sh::kStage);
 #pragma unroll
-              for (int x = 0; x < KH; ++x)
-                tma_load_3d(smem_addr(dst) + x * 8192, &kmap, x * 128, 0, block, smem_addr(&full[st]), once);
-              bulk_load(dst + kKvPage * D, a.kv.v + (size_t)block * kKvPage * D, kKvPage * D, &full[st], once);
+                for (int x = 0; x < KH; ++x)
+                  tma_load_3d(smem_addr(dst) + x * 8192, &kmap, x * 128, 0, block, smem_addr(&full[st]), once);
+                bulk_load(dst + kKvPage * D, a.kv.v + (size_t)block * kKvPage * D, kKvPage * D, &full[st], once);
+              }
+              done = true;
+            }
+            if (__all_sync(0xffffffffu, done)) break;
+            if ((it & 255u) == 0) {
+              const uint64_t t = global_ns();
+              if (t0 == 0) t0 = t;
+              const bool late = t - t0 > kWaitLimitNs;
+              if (late) {
+                atomicExch(a.kv.err, kDevErrTimeout);
+                *reinterpret_cast<volatile int*>(&abort_s) = 1;
+              }
+              alive = !__any_sync(0xffffffffu, late || *reinterpret_cast<volatile int*>(&abort_s) != 0);
+              if (!alive) break;
             }
           }
-          __syncwarp();
-          ++count;
+          if (done) last = i + 1;
         }
+        count += here;
       }
       u = p.split ? u + (s.k1 - s.k0) : u + 1;
     }
-    if (abort_s) {
+    if (*reinterpret_cast<volatile int*>(&abort_s)) {
       // drain: no copy may land after the CTA has gone
-      for (uint32_t c = count > ns ? count - ns : 0; c < count; ++c) {
+      for (uint32_t c = last > 32 ? last - 32 : 0; c < last; ++c) {
+        if (*reinterpret_cast<volatile uint32_t*>(&meta[c % ns].seq) != c + 1) continue;  // the stage's latest page only
         const uint64_t t0 = global_ns();
         while (!mbar_try_wait(&full[c % ns], (c / ns) & 1))
           if (global_ns() - t0 > kWaitLimitNs) break;
@@ -516,9 +537,10 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
         for (int c = 0; c < 4; ++c) o[nt][i][c] = 0.f;
     }
 
+    uint32_t st = (count + warp) % ns, phase = ((count + warp) / ns) & 1;
     for (int k = warp; k < n_pages && alive; k += W) {
-      const uint32_t i = count + k, st = i % ns;
-      alive = wait_page(&meta[st], &full[st], i, (i / ns) & 1, &abort_s, a.kv.err);
+      const uint32_t i = count + k;
+      alive = wait_page(&meta[st], &full[st], i, phase, &abort_s, a.kv.err);
       alive = __all_sync(0xffffffffu, alive);
       if (!alive) break;
       const StageMeta mt = meta[st];
@@ -526,39 +548,43 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
         const uint32_t kp = smem_addr(ring) + st * Sh::kStage, vp = kp + kKvPage * D;
         const bool whole = page_whole(a, t, mt.base);
         // S^T, tokens 16 (r / 2) + 2 u + r % 2 in rows, u = 2 mt and 2 mt + 1
+        // (four independent accumulators in turn: a product waits for none)
         float sacc[NT][4][4];
 #pragma unroll
-        for (int mi = 0; mi < 4; ++mi) {
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+          for (int mi = 0; mi < 4; ++mi)
 #pragma unroll
             for (int c = 0; c < 4; ++c) sacc[nt][mi][c] = 0.f;
-          const int t0 = 16 * (r >> 1) + 4 * mi + (r & 1), t1 = t0 + 2;
+        const int t_row = 16 * (r >> 1) + (r & 1);
 #pragma unroll
-          for (int x = 0; x < KH; ++x)
+        for (int x = 0; x < KH; ++x)
 #pragma unroll
-            for (int c = 0; c < KC; ++c) {
-              uint4 v0, v1;
-              if constexpr (D == 64) {
-                v0 = lds128(kp + t0 * 64 + 16 * j);
-                v1 = lds128(kp + t1 * 64 + 16 * j);
-              } else {
-                v0 = lds128(kp + x * 8192 + t0 * 128 + (((2 * j + c) ^ (t0 & 7)) << 4));
-                v1 = lds128(kp + x * 8192 + t1 * 128 + (((2 * j + c) ^ (t1 & 7)) << 4));
+          for (int c = 0; c < KC; ++c) {
+            uint4 v[4][2];
+#pragma unroll
+            for (int mi = 0; mi < 4; ++mi)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const int t = t_row + 4 * mi + 2 * h;
+                v[mi][h] = D == 64 ? lds128(kp + t * 64 + 16 * j)
+                                   : lds128(kp + x * 8192 + t * 128 + (((2 * j + c) ^ (t & 7)) << 4));
               }
-              const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
 #pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const uint32_t af[4] = {e4m3x2_to_f16x2(w0[q] & 0xffffu), e4m3x2_to_f16x2(w1[q] & 0xffffu),
-                                        e4m3x2_to_f16x2(w0[q] >> 16), e4m3x2_to_f16x2(w1[q] >> 16)};
-                const int ks = (x * KC + c) * 4 + q;
+            for (int q = 0; q < 4; ++q) {
+              const int ks = (x * KC + c) * 4 + q;
+#pragma unroll
+              for (int mi = 0; mi < 4; ++mi) {
+                uint32_t af[4];
+                e4m3x4_to_f16x4(word(v[mi][0], q), af[0], af[2]);
+                e4m3x4_to_f16x4(word(v[mi][1], q), af[1], af[3]);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                   for (int pt = 0; pt < NP; ++pt) mma_f16(sacc[nt][mi], af, qf[nt][pt][ks][0], qf[nt][pt][ks][1]);
               }
             }
-        }
+          }
         // weights
         uint32_t pf[NT][NP][8];
         float alpha[NT][2];
@@ -622,37 +648,52 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
 #pragma unroll
               for (int c = 0; c < 4; ++c) o[nt][i2][c] *= alpha[nt][c & 1];
         }
-        // O^T += V^T P^T
+        // O^T += V^T P^T, four output tiles in turn
+        constexpr int G = NT == 2 ? 2 : 4;
 #pragma unroll
-        for (int md = 0; md < MD; ++md) {
-          const uint4 v0 = lds128(vp + (16 * md + r) * 64 + 16 * j), v1 = lds128(vp + (16 * md + r + 8) * 64 + 16 * j);
-          const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
-          float acc[NT][4];
+        for (int m0 = 0; m0 < MD; m0 += G) {
+          uint4 v[G][2];
+          float acc[G][NT][4];
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) acc[nt][c] = 0.f;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t af[4] = {e4m3x2_to_f16x2(w0[q] & 0xffffu), e4m3x2_to_f16x2(w1[q] & 0xffffu),
-                              e4m3x2_to_f16x2(w0[q] >> 16), e4m3x2_to_f16x2(w1[q] >> 16)};
-            if (!whole) {
-#pragma unroll
-              for (int c = 0; c < 4; ++c) af[c] = no_nan(af[c]);
-            }
+          for (int i = 0; i < G; ++i) {
+            v[i][0] = lds128(vp + (16 * (m0 + i) + r) * 64 + 16 * j);
+            v[i][1] = lds128(vp + (16 * (m0 + i) + r + 8) * 64 + 16 * j);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int pt = 0; pt < NP; ++pt) mma_f16(acc[nt], af, pf[nt][pt][2 * q], pf[nt][pt][2 * q + 1]);
+              for (int c = 0; c < 4; ++c) acc[i][nt][c] = 0.f;
           }
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+          for (int q = 0; q < 4; ++q)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) o[nt][md][c] = fmaf(acc[nt][c], mt.v_scale, o[nt][md][c]);
+            for (int i = 0; i < G; ++i) {
+              uint32_t af[4];
+              e4m3x4_to_f16x4(word(v[i][0], q), af[0], af[2]);
+              e4m3x4_to_f16x4(word(v[i][1], q), af[1], af[3]);
+              if (!whole) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) af[c] = no_nan(af[c]);
+              }
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int pt = 0; pt < NP; ++pt) mma_f16(acc[i][nt], af, pf[nt][pt][2 * q], pf[nt][pt][2 * q + 1]);
+            }
+#pragma unroll
+          for (int i = 0; i < G; ++i)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int c = 0; c < 4; ++c) o[nt][m0 + i][c] = fmaf(acc[i][nt][c], mt.v_scale, o[nt][m0 + i][c]);
         }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive_local(smem_addr(&empty[st]));
+      st += W;
+      while (st >= ns) {
+        st -= ns;
+        phase ^= 1;
+      }
     }
     count += n_pages;
 

@@ -376,10 +376,7 @@ __device__ __forceinline__ void widen16(const uint4& v, uint32_t a0, uint32_t a1
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   uint32_t f[8];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = e4m3x2_to_f16x2(w[i] & 0xffffu);
-    f[2 * i + 1] = e4m3x2_to_f16x2(w[i] >> 16);
-  }
+  for (int i = 0; i < 4; ++i) e4m3x4_to_f16x4(w[i], f[2 * i], f[2 * i + 1]);
   sts128(a0, f[0], f[1], f[2], f[3]);
   sts128(a1, f[4], f[5], f[6], f[7]);
 }
