@@ -9,6 +9,7 @@
 // the page copies move real bytes.
 #include <climits>
 #include <cmath>
+#include <cstring>
 
 #include "np.h"
 #include "np_kv.cuh"
@@ -348,13 +349,15 @@ __global__ void __launch_bounds__(kPageThreads, 1) compact_kernel(const KvPool p
 }
 
 // ---- append ---------------------------------------------------------------------------
-// One CTA per (page that gets new tokens, head).  It reads the new tokens'
-// values of that page once into registers, takes the largest magnitude,
-// raises the page's scale if needed, and writes the codes: keys token by
-// token, values through shared memory into the transposed page.  Codes that
-// were there are read again only if the scale changed.
+// One CTA per (page that gets new tokens, head), heads next to each other so
+// that neighbouring CTAs read neighbouring memory (with the pages next to each
+// other instead, 16 k tokens of 32 heads took 232 us).  A thread holds 8
+// elements of 4 tokens that share a word of the transposed page, as they came
+// (values, then keys: with both at once fewer CTAs fit an SM, 138 us against
+// 101 with six CTAs); it takes the largest magnitude, the CTA raises the page's scale if needed, and the codes go out:
+// keys token by token, values as words of 4 tokens through shared memory.
+// Codes that were there are read again only if the scale changed.
 // Bound by HBM for prompts: 2 (f32: 4) bytes read and 1 written per element.
-constexpr int kAppendThreads = 128;
 
 struct KvAppend {
   KvView kv;
@@ -362,7 +365,7 @@ struct KvAppend {
   const void* k;
   const void* v;
   long long k_tok, k_head, v_tok, v_head;
-  int direct;  // no sequence has more than one new token: CTA x = sequence x
+  int direct;  // no sequence has more than one new token: the unit is the sequence
 };
 
 // Smallest e in [-40, 40] with amax <= 448 * 2^e (448 = 1.75 * 2^8).
@@ -384,43 +387,59 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float r) {
   return f32x2_to_e4m3x2(a.x * r, a.y * r) | (f32x2_to_e4m3x2(b.x * r, b.y * r) << 16);
 }
 
-template <typename T, bool VEC>
-__device__ __forceinline__ void load8(const T* src, float* f) {
-  if constexpr (VEC) {
-    constexpr int N = 8 / Elem<T>::E;
+// 8 elements as they lie in memory.
+template <typename T> struct Raw8 {
+  static constexpr int N = 8 / Elem<T>::E;
+  uint4 r[N];
+  __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int i = 0; i < N; ++i) Elem<T>::load(reinterpret_cast<const uint4*>(src)[i], f + i * Elem<T>::E);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = kv_to_float<T>(src[i]);
+    for (int i = 0; i < N; ++i) r[i] = make_uint4(0, 0, 0, 0);
   }
-}
+  template <bool VEC> __device__ __forceinline__ void load(const T* src) {
+    if constexpr (VEC) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) r[i] = reinterpret_cast<const uint4*>(src)[i];
+    } else {
+      T one[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) one[i] = src[i];
+      memcpy(r, one, sizeof(r));
+    }
+  }
+  __device__ __forceinline__ void get(float* f) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) Elem<T>::load(r[i], f + i * Elem<T>::E);
+  }
+};
+
+template <int D> constexpr int append_threads() { return D == 256 ? 256 : 128; }
 
 template <typename T, int D, bool VEC>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(const KvAppend a) {
-  constexpr int CH = D / 8;                                // chunks of 8 elements per token
-  constexpr int PER = kKvPage * CH / kAppendThreads;       // chunks per thread
-  constexpr int VROW = kKvPage + 4;                        // padded row of the transposed codes
-  __shared__ __align__(16) uint8_t vt[D * VROW];
-  __shared__ float red[kAppendThreads / 32];
+__global__ void __launch_bounds__(append_threads<D>(), D == 256 ? 3 : 6) append_kernel(const KvAppend a) {
+  constexpr int TH = append_threads<D>(), NW = TH / 32;
+  constexpr int CH = D / 8;                // groups of 8 elements in a token
+  constexpr int G = 16 * CH / TH;          // (word of 4 tokens, 8 elements) per thread
+  __shared__ uint32_t vt[D * 16];          // transposed codes, word w of element d at w ^ (d / 8 % 16)
+  __shared__ float red[NW];
   __shared__ int nan_s[kKvPage];
-  __shared__ int item_s[4];
-  const int tid = threadIdx.x, h = blockIdx.y;
+  __shared__ int item_s[2];
+  const int tid = threadIdx.x, h = blockIdx.x % a.kv.H;
+  const int unit = blockIdx.x / a.kv.H;
   if (*a.kv.err != 0) return;
 
   // which sequence and page
   KvSeq s;
   int slot;
   if (a.direct) {
-    s = kv_seq(a.kv, a.batch, blockIdx.x);
+    s = kv_seq(a.kv, a.batch, unit);
     if (s.n < 1 || s.n > s.len) return;
     slot = (s.len - 1) / kKvPage;
   } else {
     if (tid == 0) item_s[0] = -1;
     __syncthreads();
-    // pages touched, summed over the sequences; this CTA is the blockIdx.x-th
+    // pages touched, summed over the sequences; this CTA does the unit-th
     int before = 0;
-    for (int base = 0; base < a.batch.n_seqs; base += kAppendThreads) {
+    for (int base = 0; base < a.batch.n_seqs; base += TH) {
       const int i = base + tid;
       int pages = 0;
       if (i < a.batch.n_seqs) {
@@ -438,14 +457,14 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const KvAppend a
       __syncthreads();
       int first = before + x - pages, sum = 0;
 #pragma unroll
-      for (int w = 0; w < kAppendThreads / 32; ++w) {
+      for (int w = 0; w < NW; ++w) {
         const int t = __float_as_int(red[w]);
         if (w < (tid >> 5)) first += t;
         sum += t;
       }
-      if (pages && (int)blockIdx.x >= first && (int)blockIdx.x < first + pages) {
+      if (pages && unit >= first && unit < first + pages) {
         item_s[0] = i;
-        item_s[1] = (int)blockIdx.x - first;
+        item_s[1] = unit - first;
       }
       before += sum;
     }
@@ -454,83 +473,104 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const KvAppend a
     s = kv_seq(a.kv, a.batch, item_s[0]);
     slot = (s.len - s.n) / kKvPage + item_s[1];
   }
-  const int start = s.len - s.n;                                     // position of the first new token
+  const int start = s.len - s.n;                                        // position of the first new token
   const int off = start > slot * kKvPage ? start - slot * kKvPage : 0;  // first new token in the page
   const int end = s.len - slot * kKvPage < kKvPage ? s.len - slot * kKvPage : kKvPage;
-  const int m = end - off;
-  const int tok0 = s.begin + slot * kKvPage + off - start;  // its place in the call's tensors
+  const int tok0 = s.begin + slot * kKvPage - start;  // place of the page's token 0 in the call's tensors
   const int page = a.kv.table[(size_t)s.row * a.kv.max_pages + slot];
   if (page < 0 || page >= a.kv.n_pages || a.kv.refs[page] != 1) {
     if (tid == 0) atomicExch(a.kv.err, kDevErrBounds);
     return;
   }
   const size_t block = (size_t)page * a.kv.H + h;
-  for (int t = tid; t < kKvPage; t += kAppendThreads) nan_s[t] = 0;
-  __syncthreads();
+  for (int t = tid; t < kKvPage; t += TH) nan_s[t] = 0;
 
-#pragma unroll 1
-  for (int side = 0; side < 2; ++side) {  // 0: values (their NaNs mark the keys), 1: keys
-    const T* src = side == 0 ? static_cast<const T*>(a.v) + (long long)h * a.v_head + (long long)tok0 * a.v_tok
-                             : static_cast<const T*>(a.k) + (long long)h * a.k_head + (long long)tok0 * a.k_tok;
+  // group g of this thread: tokens 4 w .. 4 w + 3, elements d .. d + 7
+  auto word_of = [&](int g) { return (g * TH + tid) / CH; };
+  const int d = tid % CH * 8;
+  auto load = [&](int side, Raw8<T> (&x)[G][4]) {
+    const T* src = side == 0 ? static_cast<const T*>(a.v) + (long long)h * a.v_head + d
+                             : static_cast<const T*>(a.k) + (long long)h * a.k_head + d;
     const long long stride = side == 0 ? a.v_tok : a.k_tok;
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int t = 4 * word_of(g) + i;
+        if (t >= off && t < end) x[g][i].template load<VEC>(src + (long long)(tok0 + t) * stride);
+        else x[g][i].clear();
+      }
+  };
+  // side 0: values (their NaNs mark the keys), 1: keys
+  auto write = [&](int side, const Raw8<T> (&x)[G][4]) {
     float* scale_p = (side == 0 ? a.kv.v_scale : a.kv.k_scale) + block;
     uint8_t* codes = (side == 0 ? a.kv.v : a.kv.k) + block * kKvPage * D;
-    float x[PER][8];
+    const float had = off > 0 ? *scale_p : 0.f;  // a page's first token starts it afresh
     float top = 0.f;
 #pragma unroll
-    for (int c = 0; c < PER; ++c) {
-      const int t = (c * kAppendThreads + tid) / CH, d = (c * kAppendThreads + tid) % CH * 8;
-      if (t < m) {
-        load8<T, VEC>(src + t * stride + d, x[c]);
+    for (int g = 0; g < G; ++g)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[c][e]));  // fmaxf passes over a NaN
+      for (int i = 0; i < 4; ++i) {
+        float f[8];
+        x[g][i].get(f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[e]));  // fmaxf passes over a NaN
       }
-    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    __syncthreads();
+    __syncthreads();  // red is free; everyone has read the old scale of this side, nan_s is clear
     if ((tid & 31) == 0) red[tid >> 5] = top;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kAppendThreads / 32; ++w) top = fmaxf(top, red[w]);
-    const float need = pow2f(scale_exponent(top));
-    const float had = off > 0 ? *scale_p : 0.f;  // a page's first token starts it afresh
-    const float now = fmaxf(need, had);
+    for (int w = 0; w < NW; ++w) top = fmaxf(top, red[w]);
+    const float now = fmaxf(pow2f(scale_exponent(top)), had);
     const bool grown = off > 0 && now != had;
     const float inv = 1.f / now, ratio = had * inv;
-    __syncthreads();  // everyone has read the old scale
     if (tid == 0) *scale_p = now;
 #pragma unroll
-    for (int c = 0; c < PER; ++c) {
-      const int t = (c * kAppendThreads + tid) / CH, d = (c * kAppendThreads + tid) % CH * 8;
-      if (t >= m) continue;
-      float* y = x[c];
-      if (side == 0) {
-        bool nan = false;
+    for (int g = 0; g < G; ++g) {
+      const int w = word_of(g);
+      uint32_t c[4][2];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          nan |= isnan(y[e]);
-          y[e] = isnan(y[e]) ? 0.f : y[e] * inv;
+      for (int i = 0; i < 4; ++i) {
+        const int t = 4 * w + i;
+        float f[8];
+        x[g][i].get(f);
+        if (side == 0) {
+          bool nan = false;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            nan |= isnan(f[e]);
+            f[e] = isnan(f[e]) ? 0.f : f[e] * inv;
+          }
+          if (nan) nan_s[t] = 1;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] *= inv;
+          if (d == 0 && nan_s[t]) f[0] = __int_as_float(0x7fffffff);
         }
-        if (nan) nan_s[t] = 1;
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] *= inv;
-        if (d == 0 && nan_s[t]) y[0] = __int_as_float(0x7fffffff);
+        c[i][0] = f32x2_to_e4m3x2(f[0], f[1]) | (f32x2_to_e4m3x2(f[2], f[3]) << 16);
+        c[i][1] = f32x2_to_e4m3x2(f[4], f[5]) | (f32x2_to_e4m3x2(f[6], f[7]) << 16);
+        if (side == 1 && t >= off && t < end)
+          *reinterpret_cast<uint2*>(codes + t * D + d) = make_uint2(c[i][0], c[i][1]);
       }
-      uint2 w;
-      w.x = f32x2_to_e4m3x2(y[0], y[1]) | (f32x2_to_e4m3x2(y[2], y[3]) << 16);
-      w.y = f32x2_to_e4m3x2(y[4], y[5]) | (f32x2_to_e4m3x2(y[6], y[7]) << 16);
-      if (side == 1) {
-        *reinterpret_cast<uint2*>(codes + (off + t) * D + d) = w;
-      } else {
+      if (side == 0) {
+        // 4 x 4 bytes turned over, twice
 #pragma unroll
-        for (int e = 0; e < 8; ++e) vt[(d + e) * VROW + off + t] = (uint8_t)((e < 4 ? w.x : w.y) >> (8 * (e & 3)));
+        for (int q = 0; q < 2; ++q) {
+          const uint32_t x01 = __byte_perm(c[0][q], c[1][q], 0x5140), x23 = __byte_perm(c[2][q], c[3][q], 0x5140);
+          const uint32_t y01 = __byte_perm(c[0][q], c[1][q], 0x7362), y23 = __byte_perm(c[2][q], c[3][q], 0x7362);
+          uint32_t* row = vt + (d + 4 * q) * 16 + (w ^ (d / 8 % 16));
+          row[0] = __byte_perm(x01, x23, 0x5410);
+          row[16] = __byte_perm(x01, x23, 0x7632);
+          row[32] = __byte_perm(y01, y23, 0x5410);
+          row[48] = __byte_perm(y01, y23, 0x7632);
+        }
       }
     }
     if (side == 1) {
       if (grown)
-        for (int i = tid; i < off * D / 4; i += kAppendThreads) {
+        for (int i = tid; i < off * D / 4; i += TH) {
           uint32_t* p = reinterpret_cast<uint32_t*>(codes) + i;
           *p = rescale4(*p, ratio);
         }
@@ -538,12 +578,11 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const KvAppend a
       __syncthreads();
       // words of 4 tokens: whole new ones are written, others merged with
       // what is there (rescaled before the first new token if the scale grew)
-      const int w0 = grown ? 0 : off / 4, w1 = (end + 3) / 4;
-      const int nw = w1 - w0;
-      for (int i = tid; i < nw * D; i += kAppendThreads) {
-        const int d = i / nw, w = w0 + i % nw;
-        uint32_t* p = reinterpret_cast<uint32_t*>(codes + d * kKvPage) + w;
-        uint32_t fresh = *reinterpret_cast<const uint32_t*>(vt + d * VROW + 4 * w);
+      const int w0 = grown ? 0 : off / 4, nw = (end + 3) / 4 - w0;
+      for (int i = tid; i < nw * D; i += TH) {
+        const int e = i / nw, w = w0 + i % nw;
+        uint32_t* p = reinterpret_cast<uint32_t*>(codes + e * kKvPage) + w;
+        uint32_t fresh = vt[e * 16 + (w ^ (e / 8 % 16))];
         if (4 * w < off || 4 * w + 4 > end) {
           const uint32_t old = *p, scaled = grown ? rescale4(old, ratio) : old;
           uint32_t r = 0;
@@ -556,9 +595,13 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const KvAppend a
         }
         *p = fresh;
       }
-      __syncthreads();
     }
-  }
+  };
+  Raw8<T> x[G][4];
+  load(0, x);
+  write(0, x);
+  load(1, x);
+  write(1, x);
 }
 
 // ---- host side -------------------------------------------------------------------------
@@ -647,23 +690,20 @@ np_status copy_pages(const np_kv_desc* d, long long most, int remap, cudaStream_
   return launched(call);
 }
 
-template <typename T>
-cudaError_t launch_append(const KvAppend& a, int items, bool vec, cudaStream_t st) {
-  const dim3 grid((unsigned)items, (unsigned)a.kv.H);
-  switch (a.kv.D) {
-    case 64:
-      if (vec) append_kernel<T, 64, true><<<grid, kAppendThreads, 0, st>>>(a);
-      else append_kernel<T, 64, false><<<grid, kAppendThreads, 0, st>>>(a);
-      break;
-    case 128:
-      if (vec) append_kernel<T, 128, true><<<grid, kAppendThreads, 0, st>>>(a);
-      else append_kernel<T, 128, false><<<grid, kAppendThreads, 0, st>>>(a);
-      break;
-    default:
-      if (vec) append_kernel<T, 256, true><<<grid, kAppendThreads, 0, st>>>(a);
-      else append_kernel<T, 256, false><<<grid, kAppendThreads, 0, st>>>(a);
-  }
+template <typename T, int D>
+cudaError_t launch_append(const KvAppend& a, unsigned grid, bool vec, cudaStream_t st) {
+  if (vec) append_kernel<T, D, true><<<grid, append_threads<D>(), 0, st>>>(a);
+  else append_kernel<T, D, false><<<grid, append_threads<D>(), 0, st>>>(a);
   return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_append(const KvAppend& a, long long items, bool vec, cudaStream_t st) {
+  if (items * a.kv.H > INT_MAX) return cudaErrorInvalidValue;
+  const unsigned grid = (unsigned)(items * a.kv.H);
+  return a.kv.D == 64    ? launch_append<T, 64>(a, grid, vec, st)
+         : a.kv.D == 128 ? launch_append<T, 128>(a, grid, vec, st)
+                         : launch_append<T, 256>(a, grid, vec, st);
 }
 
 }  // namespace
@@ -750,7 +790,7 @@ extern "C" np_status np_kv_append(const np_kv_desc* d, int32_t layer, const np_k
   // pages touched by n sequences with N new tokens together: at most
   // min(N, N / 64 + 2 n)
   const long long most = (long long)b->n_tokens / kKvPage + 2ll * b->n_seqs;
-  const int items = a.direct ? b->n_seqs : (int)(most < b->n_tokens ? most : b->n_tokens);
+  const long long items = a.direct ? b->n_seqs : most < b->n_tokens ? most : b->n_tokens;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e = dtype == NP_F32   ? launch_append<float>(a, items, vec, st)
                         : dtype == NP_F16 ? launch_append<__half>(a, items, vec, st)

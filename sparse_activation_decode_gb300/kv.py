@@ -22,6 +22,12 @@ from . import _lib as L
 PAGE = 64  # tokens per page and per scale (NP_KV_PAGE)
 _DTYPES = {torch.float32: L.NP_F32, torch.float16: L.NP_F16, torch.bfloat16: L.NP_BF16}
 
+# the raw forms of torch.cuda.current_device / current_stream (a few hundred
+# nanoseconds instead of microseconds)
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+_current_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
 
 class KvCache:
     """Keys and values of `n_layers` layers in e4m3, in pages of 64 tokens with
@@ -95,26 +101,33 @@ class KvCache:
                                               self._work.data_ptr())
         self.desc = d
         self._desc = ctypes.byref(d)
+        self._index = self.device.index
+        self._scale = 1.0 / math.sqrt(dim)
         self._ws_bytes = {}  # workspace sizes by (heads, most new tokens, dtype)
 
-    # -- argument checks -----------------------------------------------------
+    # -- argument checks (short: a decode step makes these calls per layer) -----
     def _stream(self) -> int:
-        if torch.cuda.current_device() != self.device.index:
+        if _current_device() != self._index:
             raise ValueError(f"the cache lives on {self.device}; make it the current device")
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream(self._index)
 
     def _ints(self, t: torch.Tensor, what: str, n: int | None = None) -> int:
-        if (t.dtype != torch.int32 or t.device != self.device or t.dim() != 1 or not t.is_contiguous()
+        if (t.dtype != torch.int32 or t.get_device() != self._index or t.dim() != 1 or not t.is_contiguous()
                 or (n is not None and t.shape[0] != n) or not 1 <= t.shape[0] <= L.NP_KV_MAX_BATCH + 1):
             raise ValueError(f"{what} must be a contiguous int32 vector on {self.device}"
                              + ("" if n is None else f" of {n} elements"))
         return t.data_ptr()
 
     def _tokens(self, t: torch.Tensor, heads: int | None, what: str):
-        if (t.dim() != 3 or t.shape[2] != self.head_dim or t.dtype not in _DTYPES or t.device != self.device
-                or (heads is not None and t.shape[1] != heads) or (t.stride(2) != 1 and t.numel())):
-            raise ValueError(f"{what} must be [tokens][heads][{self.head_dim}] float32, float16 or bfloat16 on "
-                             f"{self.device}, the last dimension contiguous")
+        """(tokens, heads, token stride, head stride, dtype code) of a token-major tensor."""
+        code = _DTYPES.get(t.dtype)
+        if code is not None and t.dim() == 3 and t.get_device() == self._index:
+            n, h, d = t.shape
+            s0, s1, s2 = t.stride()
+            if d == self.head_dim and (heads is None or h == heads) and (s2 == 1 or n == 0):
+                return n, h, s0, s1, code
+        raise ValueError(f"{what} must be [tokens][{'heads' if heads is None else heads}][{self.head_dim}] float32, "
+                         f"float16 or bfloat16 on {self.device}, the last dimension contiguous")
 
     def _batch(self, n_tokens: int, cu, seqs, max_tokens):
         if seqs is not None:
@@ -169,13 +182,13 @@ class KvCache:
         same number.  `max_new`: no sequence has more (1 selects the
         single-token launch)."""
         st = self._stream()
-        self._tokens(k, self.n_kv_heads, "k")
-        self._tokens(v, self.n_kv_heads, "v")
-        if k.shape[0] != v.shape[0] or k.dtype != v.dtype:
+        n, _, k0, k1, code = self._tokens(k, self.n_kv_heads, "k")
+        nv, _, v0, v1, code_v = self._tokens(v, self.n_kv_heads, "v")
+        if n != nv or code != code_v:
             raise ValueError("k and v must have the same tokens and dtype")
-        b = self._batch(k.shape[0], cu, seqs, max_new)
-        L.check(self.lib.np_kv_append(self._desc, layer, ctypes.byref(b), k.data_ptr(), k.stride(0), k.stride(1),
-                                      v.data_ptr(), v.stride(0), v.stride(1), _DTYPES[k.dtype], st), "np_kv_append")
+        b = self._batch(n, cu, seqs, max_new)
+        L.check(self.lib.np_kv_append(self._desc, layer, ctypes.byref(b), k.data_ptr(), k0, k1, v.data_ptr(), v0, v1,
+                                      code, st), "np_kv_append")
 
     def attend(self, layer: int, q: torch.Tensor, cu: torch.Tensor | None = None, seqs: torch.Tensor | None = None,
                max_q: int | None = None, scale: float | None = None, window: int = 0, sinks: int = 0,
@@ -186,27 +199,25 @@ class KvCache:
         heads / kv heads.  `scale` defaults to 1/sqrt(dim).  Returns `out`
         (default: a new tensor like q); rows of no sequence are left alone."""
         st = self._stream()
-        self._tokens(q, None, "q")
+        n, heads, q0, q1, code = self._tokens(q, None, "q")
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        else:
-            self._tokens(out, q.shape[1], "out")
-            if out.shape[0] != q.shape[0] or out.dtype != q.dtype:
-                raise ValueError("out must have q's shape and dtype")
-            if q.numel() and _spans_overlap(q, out):
-                raise ValueError("out may not share memory with q")
-        b = self._batch(q.shape[0], cu, seqs, max_q)
-        key = (q.shape[1], b.max_tokens, q.dtype)
+            out = torch.empty_like(q)
+        elif n and _spans_overlap(q, out):
+            raise ValueError("out may not share memory with q")
+        if out.dtype != q.dtype or out.shape != q.shape:
+            raise ValueError("out must have q's shape and dtype")
+        _, _, o0, o1, _ = self._tokens(out, heads, "out")
+        b = self._batch(n, cu, seqs, max_q)
+        key = (heads, b.max_tokens, code)
         n_ws = self._ws_bytes.get(key)
         if n_ws is None:
-            n_ws = self.lib.np_kv_attend_workspace(self._desc, q.shape[1], b.max_tokens, _DTYPES[q.dtype])
+            n_ws = self.lib.np_kv_attend_workspace(self._desc, heads, b.max_tokens, code)
             if n_ws < 0:
-                raise ValueError(f"{q.shape[1]} query heads over {self.n_kv_heads} key heads are not supported")
+                raise ValueError(f"{heads} query heads over {self.n_kv_heads} key heads are not supported")
             self._ws_bytes[key] = n_ws
-        ws = torch.empty(n_ws, dtype=torch.uint8, device=q.device)
-        t = L.KvAttn(q.data_ptr(), out.data_ptr(), q.stride(0), q.stride(1), out.stride(0), out.stride(1),
-                     ws.data_ptr(), n_ws, q.shape[1], _DTYPES[q.dtype],
-                     1.0 / math.sqrt(self.head_dim) if scale is None else scale, window, sinks)
+        ws = torch.empty(n_ws, dtype=torch.uint8, device=self.device)
+        t = L.KvAttn(q.data_ptr(), out.data_ptr(), q0, q1, o0, o1, ws.data_ptr(), n_ws, heads, code,
+                     self._scale if scale is None else scale, window, sinks)
         L.check(self.lib.np_kv_attend(self._desc, layer, ctypes.byref(b), ctypes.byref(t), st), "np_kv_attend")
         return out
 
