@@ -350,7 +350,10 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
     }
     abort_s = 0;
     fence_barrier_init();
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&kmap)) : "memory");
   }
+  // (launched while the kernel before may still run)
+  grid_dependency_wait();
   const Plan p = plan<R>(a, gridDim.x, pre, seq, tmp);
   grid_dependents_launch();
   const long long u0 = (long long)blockIdx.x * p.chunk;
@@ -764,6 +767,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(256) attend_join_kernel(const KvAttend a) {
   constexpr int R = 8 * NT;
+  grid_dependents_launch();
   grid_dependency_wait();
   const KvCut cut = static_cast<const KvCut*>(a.ws)[blockIdx.x];
   if (cut.more == 0) return;
@@ -809,8 +813,8 @@ cudaError_t launch_stream(const KvAttend& a, cudaStream_t st) {
   auto kern = attend_stream_kernel<T, D, NT>;
   cudaError_t e = ensure_dyn_smem<StreamTag<T, D, NT>>(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
-  kern<<<ctas, Sh::kThreads, smem, st>>>(map, a, stages);
-  e = cudaGetLastError();
+  PdlConfig main(dim3((unsigned)ctas), dim3(Sh::kThreads), smem, st);
+  e = cudaLaunchKernelEx(&main.cfg, kern, map, a, stages);
   if (e != cudaSuccess) return e;
   // items too short to be cut leave no partials: a short table row, or a
   // window (pages of the window, the new tokens and the sinks, and one more

@@ -456,6 +456,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const KvAt
     tmem_relinquish();
     tc_fence_before();
   }
+  grid_dependency_wait();  // (launched while the kernel before may still run)
   const TilePlan p = tile_plan<R>(a, gridDim.x, pre, per, seq, sh.tmp);  // synchronises the CTA
   tc_fence_after();
   grid_dependents_launch();
@@ -1097,6 +1098,7 @@ template <typename T, int D>
 __global__ void __launch_bounds__(256) tile_join_kernel(const KvAttend a) {
   constexpr int R = TileShape<T, D>::R;
   constexpr int V = D / 32;  // elements per lane
+  grid_dependents_launch();
   grid_dependency_wait();
   const KvCut cut = static_cast<const KvCut*>(a.ws)[blockIdx.x];
   if (cut.more == 0) return;
@@ -1139,8 +1141,8 @@ cudaError_t launch_tile(const KvAttend& a, cudaStream_t st) {
   auto kern = attend_tile_kernel<T, D>;
   cudaError_t e = ensure_dyn_smem<TileTag<T, D>>(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
-  kern<<<ctas, kTileThreads, smem, st>>>(a);
-  e = cudaGetLastError();
+  PdlConfig main(dim3((unsigned)ctas), dim3(kTileThreads), smem, st);
+  e = cudaLaunchKernelEx(&main.cfg, kern, a);
   if (e != cudaSuccess) return e;
   PdlConfig pdl(dim3((unsigned)ctas, Sh::R / 32), dim3(256), 0, st);
   return cudaLaunchKernelEx(&pdl.cfg, tile_join_kernel<T, D>, a);
