@@ -72,6 +72,9 @@ def parse(argv=None):
                    help="oracle tokens timed for cpu_baseline (after a cold-start token; capped at ~30 s)")
     p.add_argument("--no-cpu-baseline", action="store_true")
     p.add_argument("--no-e2e", action="store_true")
+    p.add_argument("--context", type=int, default=None,
+                   help="decode with attention: every layer appends to and reads an 8-bit key/value cache that "
+                        "starts at this many tokens per sequence (one JSON line, GPU 0)")
     p.add_argument("--profile-case", action="store_true",
                    help="run the small capture case used for ncu (8-token workload of --config, 3 decode steps, "
                         "then standalone calls) and exit")
@@ -653,6 +656,77 @@ def run_cuda(args):
     return line, wl
 
 
+def run_context(args):
+    """The decode step with the other half of the layers: before each FFN the
+    layer appends this token's keys and values to an 8-bit paged cache and
+    attends over it (heads of 128; queries, keys and values are the residual
+    stream itself, since the workloads have no projections).  Reports the step
+    with attention, the same step without, and the bytes of cache read."""
+    import torch
+    from sparse_activation_decode_gb300 import KvCache, decoder_for
+    from sparse_activation_decode_gb300.build import build
+    from workloads import make_workload
+    build()
+    W, K, ctx = max(args.warmup, 3), args.steps, args.context
+    base = workload_config(args)
+    span = (base.batch - 1) * base.phase_step + 24
+    T = min(W + 2 * K, base.n_centroids - span if base.n_centroids else 10 ** 9)
+    cfg = base.replace(n_warm=0, n_decode=T, lookahead=0)
+    B, D = cfg.batch, cfg.d_model
+    dim = 128
+    heads = D // dim
+    store = torch.empty((cfg.n_sparse, cfg.d_ff, cfg.n_proj, D), dtype=cfg.torch_dtype, pin_memory=True)
+    wl = make_workload(cfg, device="cuda", store_out=store)
+    dec = decoder_for(wl, h2d_mode=args.h2d_mode)
+    xs = wl.x.to("cuda")
+    pages = -(-(ctx + W + 2 * K + 1) // 64) + 1
+    cache = KvCache(n_layers=cfg.n_layers, n_pages=B * pages, n_kv_heads=heads, head_dim=dim, max_seqs=B,
+                    max_pages=pages)
+    # the context: random codes below the NaN patterns, unit scales
+    cache.k.view(torch.uint8).random_(0, 0x60)
+    cache.v.view(torch.uint8).random_(0, 0x60)
+    cache.k_scale.fill_(2.0 ** -6)
+    cache.v_scale.fill_(2.0 ** -6)
+    cache.reserve(torch.full((B,), ctx, dtype=torch.int32, device="cuda"))
+    one = torch.ones(B, dtype=torch.int32, device="cuda")
+
+    def attend(layer, h):
+        if layer == 0:
+            cache.reserve(one)
+        x = h.view(B, heads, dim)
+        cache.append(layer, x, x)
+        x.add_(cache.attend(layer, x), alpha=0.01)
+
+    def idle(layer, h):
+        pass
+
+    def timed(mix, pos):
+        for i in range(W):
+            dec.decode_token(xs[(pos + i) % T].clone(), mix=mix)
+        hs = [xs[(pos + W + k) % T].clone() for k in range(K)]
+        ev0, ev1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        torch.cuda.synchronize()
+        ev0.record(dec.main_stream)
+        for x in hs:
+            dec.decode_token(x, mix=mix)
+        ev1.record(dec.main_stream)
+        torch.cuda.synchronize()
+        return ev0.elapsed_time(ev1) / K
+
+    ms = timed(attend, 0)
+    ms_without = timed(idle, 0)
+    cache.check()
+    dec.check_error()
+    dec.close()
+    read = 2 * B * heads * dim * cfg.n_layers * (ctx + W + K // 2)
+    print(json.dumps({
+        "metric": f"{cfg.name} decode with attention over an 8-bit cache", "value": round(B / (ms * 1e-3), 2),
+        "unit": "tok/s", "n_gpus": 1, "steps": K, "warmup": W, "ms_per_step": round(ms, 4),
+        "ms_per_step_without_attention": round(ms_without, 4), "cache_bytes_read_per_step": read,
+        "higher_is_better": True, "dtype": cfg.dtype, "data": "synthetic",
+        "config": {**config_dict(cfg, args, 1), "context": ctx, "heads": heads, "head_dim": dim}}))
+
+
 def run_oracle_tokens(wl, n_tokens, budget_s=None):
     """Decode tokens with the fp64 oracle from a cold start; returns
     (tokens timed, seconds) excluding the first (cold-start) token."""
@@ -683,6 +757,8 @@ def main():
         return profile_case(args)
     if args.impl == "reference":
         return run_reference(args)
+    if args.context is not None:
+        return run_context(args)
     res = run_cuda(args)
     if res is None:
         return

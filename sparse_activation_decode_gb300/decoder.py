@@ -138,7 +138,19 @@ class SparseDecoder:
         if cur != self.main_stream:
             cur.wait_stream(self.main_stream)
 
-    def decode_token(self, h: torch.Tensor, stats: bool = False):
+    def decode_token(self, h: torch.Tensor, stats: bool = False, mix=None):
+        """One decode step, h [batch][D] float32 updated in place.
+
+        `mix(layer, h)`, if given, is called before every layer's FFN with the
+        residual stream on the decoder's main stream (made torch's current
+        stream for the call) and adds what the rest of that layer adds, in
+        place: the attention over a KvCache, for instance.  The step is then
+        issued layer by layer (predictor after layer 0, each sparse layer's
+        reads on the side stream while earlier layers run) instead of as the
+        captured token; the per-layer predictor sees the layer's input after
+        `mix`.  `stats` and a lookahead are not available with it."""
+        if mix is not None:
+            return self._decode_mixed(h, stats, mix)
         self._on_main(h)
         st = L.Stats() if stats else None
         L.check(self.lib.np_decode_token(self.model, h.data_ptr(), ctypes.byref(st) if st else None),
@@ -147,6 +159,28 @@ class SparseDecoder:
         if st is None:
             return None
         return {k: getattr(st, k) for k, _ in L.Stats._fields_}
+
+    def _decode_mixed(self, h: torch.Tensor, stats: bool, mix) -> None:
+        if stats or self.desc.lookahead:
+            raise ValueError("decode_token with mix takes neither stats nor a lookahead")
+        if (h.dtype != torch.float32 or not h.is_cuda or not h.is_contiguous()
+                or h.numel() != self.batch * self.d_model):
+            raise ValueError("h must be a contiguous float32 CUDA tensor of batch * d_model elements")
+        shared = self.pred_kind == "shared_argmax"
+        self._on_main(h)
+        with torch.cuda.stream(self.main_stream):
+            for layer in range(self.n_layers):
+                sparse = layer >= self.n_dense
+                if sparse and shared:
+                    self.scatter(layer)
+                mix(layer, h)
+                if sparse and not shared:
+                    self.delta(self.predict(h, layer), layer)
+                    self.scatter(layer)
+                self.ffn_layers(layer, 1, h)
+                if layer == 0 and shared and self.n_sparse:
+                    self.delta(self.predict(h), -1)
+        self._back()
 
     def predict(self, h: torch.Tensor, layer: int = 0) -> torch.Tensor:
         self._on_main(h)
