@@ -22,8 +22,8 @@
 // Roles (512 threads, one CTA per SM): warps 0-3 and 4-7 the softmax of tile
 // 0 and 1 (a thread per row, no exchange between threads), warps 8-11 widen
 // the pages from global memory into the swizzled operands, warps 12
-// and 14 issue the MMAs of tile 0 and 1, warp 13 walks the work list and looks
-// up pages and scales.  S is
+// and 14 issue the products S of tile 0 and 1 and warp 15 the products P V,
+// warp 13 walks the work list and looks up pages and scales.  S is
 // held twice per tile: the products of the next page run while the weights of
 // this one are formed, so neither waits for the other's latency.  (With one S
 // of 128 keys per tile instead, a step's S -> weights -> P V -> S chain was
@@ -396,7 +396,8 @@ __device__ __forceinline__ bool rare(bool c) { return __builtin_expect(c, 0); }
 struct TileShared {
   uint64_t meta_full[kMetaSlots], meta_empty[kMetaSlots];
   uint64_t kfull[kMaxBuffers], kempty[kMaxBuffers], vfull[kMaxBuffers], vempty[kMaxBuffers];
-  uint64_t qready[2], sfull[2][2], pready[2][2], pvdone[2], drained[2];  // [tile][S buffer]
+  uint64_t qready[2], sfull[2][2], pready[2][2], pvdone[2][2];  // [tile][S buffer]
+  uint64_t drained[4];
   StepMeta meta[kMetaSlots];
   long long tmp[3];
   float fac[2][128];  // factor of each row's logits
@@ -430,24 +431,23 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const KvAt
   if (tid == 0) {
     for (int i = 0; i < kMetaSlots; ++i) {
       mbar_init(&sh.meta_full[i], 1);
-      mbar_init(&sh.meta_empty[i], 4 * NX + 4 + NX);
+      mbar_init(&sh.meta_empty[i], 4 * NX + 4 + NX + 1);
     }
     for (int i = 0; i < kMaxBuffers; ++i) {
       mbar_init(&sh.kfull[i], 4);
       mbar_init(&sh.kempty[i], NX);
       mbar_init(&sh.vfull[i], 4);
-      mbar_init(&sh.vempty[i], NX);
+      mbar_init(&sh.vempty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.qready[i], 4);
-      mbar_init(&sh.pvdone[i], 1);
       for (int j = 0; j < 2; ++j) {
         mbar_init(&sh.sfull[i][j], 1);
         mbar_init(&sh.pready[i][j], 4);
+        mbar_init(&sh.pvdone[i][j], 1);
       }
     }
-    mbar_init(&sh.drained[0], 1);
-    mbar_init(&sh.drained[1], 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&sh.drained[i], 1);
     sh.abort = 0;
     fence_barrier_init();
   }
@@ -569,119 +569,108 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const KvAt
         mbar_arrive_local(smem_addr(&sh.meta_full[count % kMetaSlots]));
       }
     }
-  } else if (warp == 12 || (NX == 2 && warp == 14)) {
-    // ---- MMA issue, one warp per tile ----
-    // The warp runs as one (every value the same in all lanes, taken through
-    // a reduction where it comes from memory) so that descriptors stay in
+  } else if (warp == 12 || (NX == 2 && warp == 14) || warp == 15) {
+    // ---- MMA issue: a warp for S of each tile, one for P V of both ----
+    // A warp runs as one (every value the same in all lanes, taken through a
+    // reduction where it comes from memory) so that descriptors stay in
     // uniform registers; the elected lane issues.  From divergent code each
-    // MMA took 75-100 cycles to issue, more than it takes to run.
-    constexpr uint32_t id_qk = idesc_f16(false, false, 128, kStepKeys);
-    constexpr uint32_t id_pv = idesc_f16(false, false, 128, D);
-    const uint32_t x = __reduce_max_sync(0xffffffffu, warp == 14);
+    // MMA took 75-100 cycles to issue, more than it takes to run, and one
+    // warp for both products of a tile was busy 2400 cycles a step.
     const uint32_t tm = __reduce_max_sync(0xffffffffu, tmem);
-    const uint32_t t_s0 = tm + Sh::S(0) + x * 128, t_o = tm + Sh::O(0) + x * D;
-    const uint64_t qd = smem_desc_sw128(q_s + x * NP * Sh::kQ, 0, 1024), kd = smem_desc_sw128(k_s, 0, 1024),
-                   vd = smem_desc_sw128(v_s, 0, 1024);
     const bool leader = elect_lane();
-    uint32_t step = 0;                  // the one whose S comes next
-    uint32_t n_s = 0, n_pv = 0, n_q = 0;  // S, P V issued, stretches begun
-    uint32_t in_stretch = 0;            // number of the current step in its stretch
-    bool mine = false, ok = true;       // the current step has rows in this tile
-    // flags of the next step, read ahead
+    // flags of entry i; 4 (no more work) when a wait has given up
     auto read_flags = [&](uint32_t i) {
       const uint32_t st = i % kMetaSlots;
+      if (!__all_sync(0xffffffffu, wait(&sh.meta_full[st], (i / kMetaSlots) & 1))) return 4u;
       const uint32_t f = __reduce_or_sync(0xffffffffu, (uint32_t)sh.meta[st].flags);
       if (leader) mbar_arrive_local(smem_addr(&sh.meta_empty[st]));
       return f;
     };
-    ok = __all_sync(0xffffffffu, wait(&sh.meta_full[0], 0));
-    uint32_t nf = ok ? read_flags(0) : 4u;
-    for (;;) {
-      const bool end = nf & 4;
-      const bool next_mine = !end && x < nf >> 8;
-      uint32_t nnf = 0;                 // flags of the step after the next
-      // within a stretch: S of the next step, then P V of this one; where a
-      // stretch ends the product comes first, since the next one's queries
-      // wait for its result to be taken
-      const bool turn = nf & 5;
-#pragma unroll 1
-      for (int o = 0; o < 2; ++o) {
-        if ((o == 0) == turn) {
-          if (step == 0) continue;
-          const uint32_t i = step - 1, vb = i % NB, buf = n_pv & 1;
-          // (every step's phase is waited for, rows or not: parity tells
-          // only the last two phases apart)
-          if (mine)
-            ok = kv_wait2(&sh.vfull[vb], (i / NB) & 1, &sh.pready[x][buf], (n_pv >> 1) & 1, abort, a.kv.err);
-          else
-            ok = wait(&sh.vfull[vb], (i / NB) & 1);
+    uint32_t nf = read_flags(0);
+    if (warp != 15) {
+      constexpr uint32_t id_qk = idesc_f16(false, false, 128, kStepKeys);
+      const uint32_t x = __reduce_max_sync(0xffffffffu, warp == 14);
+      const uint32_t t_s0 = tm + Sh::S(0) + x * 128;
+      const uint64_t qd = smem_desc_sw128(q_s + x * NP * Sh::kQ, 0, 1024), kd = smem_desc_sw128(k_s, 0, 1024);
+      uint32_t n_s = 0, n_q = 0;  // S issued, stretches begun
+      for (uint32_t step = 0; !(nf & 4); ++step) {
+        const uint32_t kb = step % NB, buf = n_s & 1;
+        const bool mine = x < nf >> 8;
+        // (every step's keys are waited for, rows or not: parity tells only
+        // the last two phases apart.)  The weights that lie in this S were
+        // read by the P V of two steps ago.
+        bool ok;
+        if (mine && n_s >= 2)
+          ok = kv_wait2(&sh.kfull[kb], (step / NB) & 1, &sh.pvdone[x][buf], ((n_s >> 1) - 1) & 1, abort, a.kv.err);
+        else
+          ok = wait(&sh.kfull[kb], (step / NB) & 1);
+        if (mine && (nf & 1)) ok = ok && wait(&sh.qready[x], n_q++ & 1);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        if (!mine) {
+          if (leader) mbar_arrive_local(smem_addr(&sh.kempty[kb]));
+        } else {
+          tc_fence_after();
+          const uint64_t bd = kd + ((kb * Sh::kKV) >> 4);
+          if (leader) {
+#pragma unroll
+            for (int pt = 0; pt < NP; ++pt)
+#pragma unroll
+              for (int k = 0; k < D / 16; ++k)
+                tc_mma(t_s0 + buf * 64, qd + ((pt * Sh::kQ + (k >> 2) * 16384u + (k & 3) * 32u) >> 4),
+                       bd + (((k >> 2) * 8192u + (k & 3) * 32u) >> 4), id_qk, pt || k);
+            tc_commit(smem_addr(&sh.sfull[x][buf]));
+            tc_commit(smem_addr(&sh.kempty[kb]));
+          }
+          __syncwarp();
+          ++n_s;
+        }
+        nf = read_flags(step + 1);
+      }
+    } else {
+      constexpr uint32_t id_pv = idesc_f16(false, false, 128, D);
+      const uint64_t vd = smem_desc_sw128(v_s, 0, 1024);
+      uint32_t n_pv[2] = {0, 0};   // P V issued
+      uint32_t in_stretch = 0;     // number of the step in its stretch
+      bool ok = true;
+      for (uint32_t step = 0; !(nf & 4); ++step) {
+        const uint32_t vb = step % NB;
+        in_stretch = nf & 1 ? 0 : in_stretch + 1;
+        const uint32_t fresh = NP == 2 ? in_stretch % kFold == 0 : in_stretch == 0;
+        const uint64_t bd = vd + ((vb * Sh::kKV) >> 4);
+        const uint32_t nx = nf >> 8;
+#pragma unroll
+        for (int x = 0; x < NX; ++x) {
+          if ((uint32_t)x >= nx) break;
+          const uint32_t buf = n_pv[x] & 1;
+          ok = x == 0 ? kv_wait2(&sh.vfull[vb], (step / NB) & 1, &sh.pready[x][buf], (n_pv[x] >> 1) & 1, abort,
+                                 a.kv.err)
+                      : wait(&sh.pready[x][buf], (n_pv[x] >> 1) & 1);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          if (!mine) {
-            if (leader) mbar_arrive_local(smem_addr(&sh.vempty[vb]));
-            continue;
-          }
           tc_fence_after();
-          const uint64_t bd = vd + ((vb * Sh::kKV) >> 4);
-          const uint32_t fresh = NP == 2 ? in_stretch % kFold == 0 : in_stretch == 0;
           if (leader) {
 #pragma unroll
             for (int pt = 0; pt < NP; ++pt)
 #pragma unroll
               for (int k = 0; k < kStepKeys / 16; ++k)
-                tc_mma_ts(t_o, t_s0 + buf * 64 + pt * 32 + k * 8, bd + ((k * 32u) >> 4), id_pv,
+                tc_mma_ts(tm + Sh::O(x), tm + Sh::S(x) + buf * 64 + pt * 32 + k * 8, bd + ((k * 32u) >> 4), id_pv,
                           (fresh ^ 1) | (pt || k));
-            tc_commit(smem_addr(&sh.pvdone[x]));
-            tc_commit(smem_addr(&sh.vempty[vb]));
+            tc_commit(smem_addr(&sh.pvdone[x][buf]));
+            if ((uint32_t)x == nx - 1) tc_commit(smem_addr(&sh.vempty[vb]));
           }
           __syncwarp();
-          ++n_pv;
-        } else {
-          if (end) continue;
-          const uint32_t kb = step % NB, buf = n_s & 1;
-          // the weights that lie in this S were read by the last P V issued (or one before it)
-          if (next_mine && n_pv)
-            ok = kv_wait2(&sh.kfull[kb], (step / NB) & 1, &sh.pvdone[x], (n_pv - 1) & 1, abort, a.kv.err);
-          else
-            ok = wait(&sh.kfull[kb], (step / NB) & 1);
-          if (next_mine && (nf & 1)) ok = ok && wait(&sh.qready[x], n_q++ & 1);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          if (!next_mine) {
-            if (leader) mbar_arrive_local(smem_addr(&sh.kempty[kb]));
-          } else {
-            tc_fence_after();
-            const uint64_t bd = kd + ((kb * Sh::kKV) >> 4);
-            if (leader) {
-#pragma unroll
-              for (int pt = 0; pt < NP; ++pt)
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k)
-                  tc_mma(t_s0 + buf * 64, qd + ((pt * Sh::kQ + (k >> 2) * 16384u + (k & 3) * 32u) >> 4),
-                         bd + (((k >> 2) * 8192u + (k & 3) * 32u) >> 4), id_qk, pt || k);
-              tc_commit(smem_addr(&sh.sfull[x][buf]));
-              tc_commit(smem_addr(&sh.kempty[kb]));
-            }
-            __syncwarp();
-            ++n_s;
-          }
-          // while these run
-          ok = __all_sync(0xffffffffu, wait(&sh.meta_full[(step + 1) % kMetaSlots], ((step + 1) / kMetaSlots) & 1));
-          if (!ok) break;
-          nnf = read_flags(step + 1);
+          ++n_pv[x];
         }
+        if (!ok) break;
+        nf = read_flags(step + 1);
       }
-      if (!ok || end) break;
-      in_stretch = nf & 1 ? 0 : in_stretch + 1;
-      mine = next_mine;
-      nf = nnf;
-      ++step;
     }
     // nothing of this CTA may be in flight when it frees the tensor memory
-    if (leader) tc_commit(smem_addr(&sh.drained[x]));
+    uint64_t* const drained = &sh.drained[warp - 12];
+    if (leader) tc_commit(smem_addr(drained));
     __syncwarp();
     const uint64_t t0 = global_ns();
-    while (!mbar_try_wait(&sh.drained[x], 0))
+    while (!mbar_try_wait(drained, 0))
       if (global_ns() - t0 > kWaitLimitNs) break;
   }
   } else if (warp >= 8) {
@@ -892,7 +881,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const KvAt
         }
         if (flags & 1) free_entry();
         if (done_flags) {
-          wait(&sh.pvdone[X], (n_steps - 1) & 1);
+          wait(&sh.pvdone[X][(n_steps - 1) & 1], ((n_steps - 1) >> 1) & 1);
           __syncwarp();
           tc_fence_after();
           const bool cut = (done_flags & 24) != 24;
@@ -1005,7 +994,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const KvAt
         }
         if (in_stretch) {
           // O rests once the last P V is done
-          wait(&sh.pvdone[X], (n_steps - 1) & 1);
+          wait(&sh.pvdone[X][(n_steps - 1) & 1], ((n_steps - 1) >> 1) & 1);
           __syncwarp();
           tc_fence_after();
 #pragma unroll 1
@@ -1066,12 +1055,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const KvAt
         }
       }
       tmem_wait_st();
-      if (rare((flags & 2) && in_stretch)) {
-        // The wait for this step's P V below can tell it from the one before
-        // by parity only once that one is done; here it cannot have begun.
-        wait(&sh.pvdone[X], (n_steps - 1) & 1);
-        __syncwarp();
-      }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_local(smem_addr(&sh.pready[X][buf]));
