@@ -461,7 +461,11 @@ np_status np_kv_compact(const np_kv_desc* kv, void* stream);
  * later token raises a page's scale the codes there are rescaled (a power of
  * two: only codes that become subnormal are rounded again).  A NaN in a key
  * is kept; a token with a NaN in its value is stored with a NaN key and that
- * element 0, so that every query that sees it gets NaN and no other does. */
+ * element 0, so that every query that sees it gets NaN and no other does.
+ * A row that is listed twice, has fewer tokens than the call brings, or names
+ * a page that it does not hold alone is not written, and NP_ERR_STATE is
+ * recorded; which of the other sequences' tokens the call still wrote is then
+ * unspecified. */
 np_status np_kv_append(const np_kv_desc* kv, int32_t layer, const np_kv_batch* batch, const void* k,
                        int64_t k_token_stride, int64_t k_head_stride, const void* v, int64_t v_token_stride,
                        int64_t v_head_stride, int32_t dtype, void* stream);
@@ -476,7 +480,8 @@ typedef struct {
   int64_t out_head_stride;
   void* workspace;           /* 16-byte aligned, for this call alone until it has run */
   int64_t workspace_bytes;   /* at least np_kv_attend_workspace() */
-  int32_t n_heads;           /* query heads: a multiple of n_kv_heads, at most 1024 */
+  int32_t n_heads;           /* query heads: a multiple of n_kv_heads, at most 1024; n_tokens *
+                                n_heads / n_kv_heads below 2^30 */
   int32_t dtype;             /* NP_F32, NP_F16 or NP_BF16 */
   float scale;               /* > 0 */
   int32_t window;            /* 0: every key up to the query's position */

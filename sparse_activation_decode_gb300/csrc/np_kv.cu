@@ -429,9 +429,11 @@ __global__ void __launch_bounds__(append_threads<D>(), D == 256 ? 3 : 6) append_
 
   // which sequence and page
   KvSeq s;
-  int slot;
+  int slot, mine;  // page of the table row, place in the call's list
   if (a.direct) {
     s = kv_seq(a.kv, a.batch, unit);
+    mine = unit;
+    if (s.n > s.len && tid == 0) atomicExch(a.kv.err, kDevErrBounds);  // more tokens than the row has room for
     if (s.n < 1 || s.n > s.len) return;
     slot = (s.len - 1) / kKvPage;
   } else {
@@ -444,6 +446,7 @@ __global__ void __launch_bounds__(append_threads<D>(), D == 256 ? 3 : 6) append_
       int pages = 0;
       if (i < a.batch.n_seqs) {
         const KvSeq t = kv_seq(a.kv, a.batch, i);
+        if (t.n > t.len) atomicExch(a.kv.err, kDevErrBounds);  // more tokens than the row has room for
         if (t.n > 0 && t.n <= t.len) pages = (t.len + kKvPage - 1) / kKvPage - (t.len - t.n) / kKvPage;
       }
       int x = pages;
@@ -470,8 +473,18 @@ __global__ void __launch_bounds__(append_threads<D>(), D == 256 ? 3 : 6) append_
     }
     __syncthreads();
     if (item_s[0] < 0) return;
-    s = kv_seq(a.kv, a.batch, item_s[0]);
+    mine = item_s[0];
+    s = kv_seq(a.kv, a.batch, mine);
     slot = (s.len - s.n) / kKvPage + item_s[1];
+  }
+  if (a.batch.seqs) {
+    // a row listed twice would be written by two CTAs at once
+    bool twice = false;
+    for (int i = tid; i < a.batch.n_seqs; i += TH) twice |= i != mine && a.batch.seqs[i] == s.row;
+    if (__syncthreads_or(twice)) {
+      if (tid == 0) atomicExch(a.kv.err, kDevErrBounds);
+      return;
+    }
   }
   const int start = s.len - s.n;                                        // position of the first new token
   const int off = start > slot * kKvPage ? start - slot * kKvPage : 0;  // first new token in the page
@@ -809,6 +822,8 @@ extern "C" np_status np_kv_attend(const np_kv_desc* d, int32_t layer, const np_k
     return kv_fail(NP_ERR_ARG, "np_kv_attend: n_heads is not a multiple of the cache's heads");
   if (!std::isfinite(t->scale) || t->scale <= 0.f || t->window < 0 || t->sinks < 0)
     return kv_fail(NP_ERR_ARG, "np_kv_attend: bad scale, window or sinks");
+  if ((int64_t)b->n_tokens * (t->n_heads / d->n_kv_heads) >= (1ll << 30))
+    return kv_fail(NP_ERR_ARG, "np_kv_attend: too many tokens for one call");
   if (b->n_tokens == 0) return NP_OK;
   const size_t esz = t->dtype == NP_F32 ? 4 : 2;
   if (!t->q || !t->out || !aligned(t->q, esz) || !aligned(t->out, esz) || t->q_token_stride < 0 ||

@@ -82,6 +82,13 @@ struct __align__(16) KvCut {
 constexpr int kKvMaxCtas = 256;  // upper bound of an attention grid
 constexpr size_t kKvCutBytes = kKvMaxCtas * sizeof(KvCut);
 
+// a / b for a >= 0, b > 0, in 32 bits where they fit (a 64-bit division takes
+// ten times as long, and every launch starts with a few).
+__device__ __forceinline__ long long kv_div(long long a, long long b) {
+  if ((((unsigned long long)a | (unsigned long long)b) >> 32) == 0) return (long long)((uint32_t)a / (uint32_t)b);
+  return a / b;
+}
+
 // Attention of one layer (np_kv_attend).
 struct KvAttend {
   KvView kv;

@@ -49,7 +49,11 @@ namespace np {
 namespace {
 
 constexpr int kMaxAttendStages = 16;
-constexpr int kTileRows = 16;       // sequences with more rows go to the tiled kernel
+// Sequences with more rows than this go to the tiled kernel (fp32, whose
+// products cost twice as much: 32).  Heads of 128, bf16, us here / tiled:
+// 8 sequences of 8000 keys, 48 rows 227 / 238, 64 rows 299 / 238; of 1500
+// keys, 32 rows 76 / 71; one of 12000, 48 rows 69 / 77, 64 rows 84 / 79.
+constexpr int kTileRows = 48, kTileRowsF32 = 32;
 constexpr int kWholePages = 8;      // items of at most this many pages are never cut
 
 template <int D> struct Shape {
@@ -122,8 +126,8 @@ __device__ __forceinline__ Plan plan(const KvAttend& a, int ctas, long long* pre
       const int l = __shfl_xor_sync(0xffffffffu, longest, o);
       longest = l > longest ? l : longest;
     }
-    const long long per = (items + ctas - 1) / ctas;
-    const bool split = longest > kWholePages && per * longest > pages / ctas + kWholePages;
+    const long long per = kv_div(items + ctas - 1, ctas);
+    const bool split = longest > kWholePages && per * longest > kv_div(pages, ctas) + kWholePages;
     const long long total = split ? pages : items;
     long long run = 0;
     for (int base = 0; base < n; base += 32) {
@@ -144,7 +148,7 @@ __device__ __forceinline__ Plan plan(const KvAttend& a, int ctas, long long* pre
     }
     if (lane == 0) {
       pre[n] = total;
-      tmp[0] = (total + ctas - 1) / ctas;
+      tmp[0] = kv_div(total + ctas - 1, ctas);
       tmp[1] = split;
     }
   }
@@ -183,9 +187,9 @@ __device__ __forceinline__ Segment segment_at(const KvAttend& a, const Plan& p, 
   const int g = a.Hq / a.kv.H;
   const int tiles = (int)((w.n * (long long)g + R - 1) / R);
   const long long off = u - pre[s.b];
-  const long long item = p.split ? off / s.pages.count : off;
-  s.h = (int)(item / tiles);
-  s.tile = (int)(item % tiles);
+  const long long item = p.split ? kv_div(off, s.pages.count) : off;
+  s.h = (int)kv_div(item, tiles);
+  s.tile = (int)(item - (long long)s.h * tiles);
   if (p.split) {
     s.k0 = (int)(off - item * s.pages.count);
     const long long left = end - u;
@@ -371,7 +375,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
       if (p.split && u0 < u1) {
         const Segment s = segment_at<R>(a, p, pre, seq, u0, p.total);
         if (!s.starts && s.k0 <= p.chunk) {  // the first cut inside this item
-          cut.more = (int)((s.pages.count - s.k0 + p.chunk - 1) / p.chunk);
+          cut.more = (int)kv_div(s.pages.count - s.k0 + p.chunk - 1, p.chunk);
           cut.row0 = s.tile * R;
           cut.rows = tile_rows<R>(a, seq[s.b], s.tile).rows;
           cut.begin = seq[s.b].begin;
@@ -850,7 +854,7 @@ int kv_attend_ctas() {
 }
 
 static bool takes_tile(int dtype, int head_dim, long long rows) {
-  return rows > kTileRows && kv_tile_takes(dtype, head_dim);
+  return rows > (dtype == 0 ? kTileRowsF32 : kTileRows) && kv_tile_takes(dtype, head_dim);
 }
 
 size_t kv_attend_workspace(int dtype, int head_dim, long long rows) {

@@ -117,10 +117,10 @@ __device__ __forceinline__ int tiles_of(const KvAttend& a, int n, int R) {
 }
 
 // Numbers the units (steps, or whole items where nothing is to be gained by
-// cutting): pre[i] = units before sequence i; per[i] = units of one head of
-// sequence i.  Called by the whole CTA.
+// cutting): pre[i] = units before sequence i, every head of a sequence having
+// as many.  Called by the whole CTA.
 template <int R>
-__device__ __forceinline__ TilePlan tile_plan(const KvAttend& a, int ctas, long long* pre, int* per, TileSeq* seq,
+__device__ __forceinline__ TilePlan tile_plan(const KvAttend& a, int ctas, long long* pre, TileSeq* seq,
                                               long long* tmp) {
   const int n = a.batch.n_seqs;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
@@ -132,7 +132,8 @@ __device__ __forceinline__ TilePlan tile_plan(const KvAttend& a, int ctas, long 
   __syncthreads();
   for (int i = warp; i < n; i += warps) {
     const int tiles = tiles_of(a, seq[i].n, R);
-    int steps = 0, longest = 0;
+    long long steps = 0;
+    int longest = 0;
     for (int t = lane; t < tiles; t += 32) {
       const int s = tile_keys<R>(a, seq[i].n, seq[i].len, t).pages;
       steps += s;
@@ -145,7 +146,7 @@ __device__ __forceinline__ TilePlan tile_plan(const KvAttend& a, int ctas, long 
       longest = l > longest ? l : longest;
     }
     if (lane == 0) {
-      per[i] = steps;
+      pre[i] = steps;
       atomicMax(reinterpret_cast<unsigned long long*>(&tmp[2]), (unsigned long long)longest);
     }
   }
@@ -154,21 +155,20 @@ __device__ __forceinline__ TilePlan tile_plan(const KvAttend& a, int ctas, long 
     long long items = 0, steps = 0;
     for (int i = lane; i < n; i += 32) {
       items += (long long)tiles_of(a, seq[i].n, R) * a.kv.H;
-      steps += (long long)per[i] * a.kv.H;
+      steps += pre[i] * a.kv.H;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       items += __shfl_xor_sync(0xffffffffu, items, o);
       steps += __shfl_xor_sync(0xffffffffu, steps, o);
     }
-    const bool split = (items + ctas - 1) / ctas * tmp[2] > steps / ctas + kCutCost;
+    const bool split = kv_div(items + ctas - 1, ctas) * tmp[2] > kv_div(steps, ctas) + kCutCost;
     long long run = 0;
     for (int base = 0; base < n; base += 32) {
       const int i = base + lane;
       long long u = 0;
       if (i < n) {
-        if (!split) per[i] = tiles_of(a, seq[i].n, R);
-        u = (long long)per[i] * a.kv.H;
+        u = (split ? pre[i] : (long long)tiles_of(a, seq[i].n, R)) * a.kv.H;
       }
       long long x = u;
 #pragma unroll
@@ -181,7 +181,7 @@ __device__ __forceinline__ TilePlan tile_plan(const KvAttend& a, int ctas, long 
     }
     if (lane == 0) {
       pre[n] = run;
-      tmp[0] = (run + ctas - 1) / ctas;
+      tmp[0] = kv_div(run + ctas - 1, ctas);
       tmp[1] = split;
     }
   }
@@ -203,7 +203,7 @@ struct TilePos {
 // Unit u (called by a whole warp).
 template <int R>
 __device__ __forceinline__ TilePos tile_find(const KvAttend& a, const TilePlan& p, const long long* pre,
-                                             const int* per, const TileSeq* seq, long long u) {
+                                             const TileSeq* seq, long long u) {
   const int lane = threadIdx.x & 31;
   int lo = 0, hi = a.batch.n_seqs;
   while (hi - lo > 1) {
@@ -213,11 +213,11 @@ __device__ __forceinline__ TilePos tile_find(const KvAttend& a, const TilePlan& 
   TilePos t;
   t.b = lo;
   t.tiles = tiles_of(a, seq[lo].n, R);
-  const long long off = u - pre[lo];
-  t.h = (int)(off / per[lo]);
-  int rem = (int)(off % per[lo]);
+  const long long off = u - pre[lo], per = kv_div(pre[lo + 1] - pre[lo], a.kv.H);
+  t.h = (int)kv_div(off, per);
+  long long rem = off - t.h * per;
   t.step = 0;
-  t.tile = rem;
+  t.tile = (int)rem;
   if (!p.split) return t;
   for (int base = 0; base < t.tiles; base += 32) {
     const int i = base + lane;
@@ -232,12 +232,12 @@ __device__ __forceinline__ TilePos tile_find(const KvAttend& a, const TilePlan& 
     if (hit) {
       const int l = __ffs(hit) - 1;
       t.tile = base + l;
-      t.step = rem - __shfl_sync(0xffffffffu, x - s, l);
+      t.step = (int)rem - __shfl_sync(0xffffffffu, x - s, l);
       return t;
     }
     rem -= __shfl_sync(0xffffffffu, x, 31);
   }
-  t.tile = t.tiles - 1;  // not reached: rem < per[lo]
+  t.tile = t.tiles - 1;  // not reached: rem < per
   return t;
 }
 
@@ -425,7 +425,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const KvAt
   const uint32_t q_s = smem_addr(ops), k_s = q_s + NX * NP * Sh::kQ, v_s = k_s + NB * Sh::kKV;
   long long* pre = reinterpret_cast<long long*>(ops + Sh::kOperands);
   TileSeq* seq = reinterpret_cast<TileSeq*>(pre + a.batch.n_seqs + 1 + ((a.batch.n_seqs + 1) & 1));
-  int* per = reinterpret_cast<int*>(seq + a.batch.n_seqs);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
@@ -457,7 +456,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const KvAt
     tc_fence_before();
   }
   grid_dependency_wait();  // (launched while the kernel before may still run)
-  const TilePlan p = tile_plan<R>(a, gridDim.x, pre, per, seq, sh.tmp);  // synchronises the CTA
+  const TilePlan p = tile_plan<R>(a, gridDim.x, pre, seq, sh.tmp);  // synchronises the CTA
   tc_fence_after();
   grid_dependents_launch();
   const uint32_t tmem = sh.tmem;
@@ -483,10 +482,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const KvAt
     };
     KvCut cut{};
     if (u0 < u1) {
-      TilePos t = tile_find<R>(a, p, pre, per, seq, u0);
+      TilePos t = tile_find<R>(a, p, pre, seq, u0);
       if (t.step > 0 && t.step <= p.chunk) {  // the first cut inside this item
         const TileKeys tk = tile_keys<R>(a, seq[t.b].n, seq[t.b].len, t.tile);
-        cut.more = (int)((tk.pages - t.step + p.chunk - 1) / p.chunk);
+        cut.more = (int)kv_div(tk.pages - t.step + p.chunk - 1, p.chunk);
         cut.row0 = t.tile * R;
         cut.rows = tk.rows;
         cut.begin = seq[t.b].begin;
@@ -1119,7 +1118,7 @@ cudaError_t launch_tile(const KvAttend& a, cudaStream_t st) {
   using Sh = TileShape<T, D>;
   const int ctas = kv_attend_ctas();
   if (ctas < 1) return cudaErrorInvalidDevice;
-  const size_t list = ((size_t)a.batch.n_seqs + 2) * 8 + (size_t)a.batch.n_seqs * (sizeof(TileSeq) + 4);
+  const size_t list = ((size_t)a.batch.n_seqs + 2) * 8 + (size_t)a.batch.n_seqs * sizeof(TileSeq);
   const size_t smem = 1024 + Sh::kOperands + list;
   auto kern = attend_tile_kernel<T, D>;
   cudaError_t e = ensure_dyn_smem<TileTag<T, D>>(reinterpret_cast<const void*>(kern), smem);

@@ -583,3 +583,74 @@ def test_the_operators_together_over_a_search():
     p.release([0, 1, 2, 3])
     p.same()
     assert int(p.c.refs.sum()) == 0
+
+
+# ---- the ends of the ranges -----------------------------------------------------
+def test_append_refuses_a_row_listed_twice_and_too_many_tokens():
+    from sparse_activation_decode_gb300 import NpError
+    p = Pair(P=8, B=4, W=2)
+    p.grow([40, 40, 5, 0])
+    k = p.c.k.clone()
+    for counts, seqs, most in (([1, 1], [1, 1], 1), ([3, 9], [0, 0], None), ([6], [2], None), ([1], [3], 1)):
+        p.c.append(0, p.tokens(sum(counts), "f16"), p.tokens(sum(counts), "f16"), cu=cu_of(counts), seqs=i32(seqs),
+                   max_new=most)
+        with pytest.raises(NpError) as e:
+            p.c.check()
+        assert e.value.status == -6
+    assert torch.equal(k.view(torch.uint8), p.c.k.view(torch.uint8))
+
+
+@pytest.mark.parametrize("counts", [[1, 1], [30, 7]], ids=["single", "prompt"])
+def test_many_query_heads_to_a_key_head(counts):
+    p = Pair(P=12, H=1, D=64, B=2, W=6)
+    p.grow([300, 129])
+    for dtype in ("f16", "f32"):
+        p.attend_close(counts, 24, dtype)
+        p.attend_close(counts, 71, dtype, window=40, sinks=2)
+
+
+@pytest.mark.parametrize("most", [1, 64])
+def test_the_largest_batch(most):
+    # 1024 sequences, most of them of a few tokens
+    p = Pair(P=1200, H=1, D=128, B=1024, W=2)
+    rng = np.random.default_rng(3)
+    counts = [int(x) for x in rng.integers(1, 4, 1024)]
+    counts[17], counts[1023] = 64, 40
+    p.grow(counts, "f16")
+    new = [min(c, most) for c in counts]
+    p.attend_close(new, 1, "f16", max_q=most)
+
+
+def test_offsets_beyond_32_bits():
+    """A cache whose pages lie beyond 4 GB gives the same bits as a small one."""
+    from sparse_activation_decode_gb300 import KvCache
+    H, D = 16, 128
+    n = 1 << 16                                            # 8.6 GB of keys, as much of values
+    big = KvCache(n_layers=1, n_pages=n, n_kv_heads=H, head_dim=D, max_seqs=3, max_pages=40)
+    small = KvCache(n_layers=1, n_pages=64, n_kv_heads=H, head_dim=D, max_seqs=3, max_pages=40)
+    big.refs[:n - 64] = 1                                   # only the last pages are free
+    counts = [1900, 3, 64]
+    k, v = (torch.randn(sum(counts), H, D, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    for c in (big, small):
+        c.reserve(i32(counts))
+        c.append(0, k, v, cu=cu_of(counts))
+    assert int(big.table[0, 0]) == n - 64
+    for m, kw in (([1, 1, 1], dict(max_q=1)), ([130, 3, 60], {})):
+        q = torch.randn(sum(m), 2 * H, D, device="cuda", dtype=torch.bfloat16)
+        a, b = (c.attend(0, q, cu=cu_of(m), **kw) for c in (big, small))
+        assert torch.equal(a, b)
+    big.fork(i32([0]), i32([1]))
+    big.reserve(i32([0, 1, 0]))                             # 1900 is no multiple of 64: the last page is copied
+    assert torch.equal(big.k[0, big.table[1, 29].long()].view(torch.uint8),
+                       big.k[0, big.table[0, 29].long()].view(torch.uint8))
+    assert int(big.table[1, 29]) != int(big.table[0, 29])
+    big.refs[:n - 64] = 0
+    big.compact()
+    a = big.attend(0, q, cu=cu_of(m))
+    assert int(big.table.max()) < 64
+    big.check()
+    # the split follows every length of the batch: the small cache takes the same steps
+    small.fork(i32([0]), i32([1]))
+    small.reserve(i32([0, 1, 0]))
+    assert torch.equal(a, small.attend(0, q, cu=cu_of(m)))
+    small.check()

@@ -97,6 +97,8 @@ def test_bad_layers_lists_and_tensors_are_refused(lib):
     for layer in (-1, 2):
         assert lib.np_kv_attend(d, layer, b, t, None) == L.NP_ERR_ARG
         assert lib.np_kv_append(d, layer, b, FAKE, 512, 128, FAKE, 512, 128, L.NP_F16, None) == L.NP_ERR_ARG
+    many = ctypes.byref(batch(n_tokens=1 << 29, max_tokens=1 << 29))
+    assert lib.np_kv_attend(d, 0, many, ctypes.byref(attn(lib, workspace_bytes=1 << 40)), None) == L.NP_ERR_ARG
     assert lib.np_kv_append(d, 0, b, None, 512, 128, FAKE, 512, 128, L.NP_F16, None) == L.NP_ERR_ARG
     assert lib.np_kv_append(d, 0, b, FAKE, 512, -128, FAKE, 512, 128, L.NP_F16, None) == L.NP_ERR_ARG
     assert lib.np_kv_append(d, 0, b, FAKE + 2, 512, 128, FAKE, 512, 128, L.NP_F32, None) == L.NP_ERR_ARG
