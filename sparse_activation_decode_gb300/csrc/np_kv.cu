@@ -352,11 +352,15 @@ __global__ void __launch_bounds__(kPageThreads, 1) compact_kernel(const KvPool p
 // One CTA per (page that gets new tokens, head), heads next to each other so
 // that neighbouring CTAs read neighbouring memory (with the pages next to each
 // other instead, 16 k tokens of 32 heads took 232 us).  A thread holds 8
-// elements of 4 tokens that share a word of the transposed page, as they came
-// (values, then keys: with both at once fewer CTAs fit an SM, 138 us against
-// 101 with six CTAs); it takes the largest magnitude, the CTA raises the page's scale if needed, and the codes go out:
-// keys token by token, values as words of 4 tokens through shared memory.
-// Codes that were there are read again only if the scale changed.
+// elements of 4 tokens that share a word of the transposed page, as they came:
+// values in registers, keys copied into shared memory meanwhile.  It takes the
+// largest magnitude, the CTA raises the page's scale if needed, and the codes
+// go out: keys token by token, values as words of 4 tokens through shared
+// memory.  Codes that were there are read again only if the scale changed.
+// 16 k tokens of 32 heads of 128, bf16: 81.5 us, 5.05 TB/s (keys loaded after
+// the values 102; a word of values at a time 99; maxima and NaN tests by
+// element 85.5; six CTAs an SM the same, eight 88).  One token of 8
+// sequences: 5.0 us, the chain lengths -> table -> holders -> elements -> scale.
 // Bound by HBM for prompts: 2 (f32: 4) bytes read and 1 written per element.
 
 struct KvAppend {
@@ -410,12 +414,48 @@ template <typename T> struct Raw8 {
 #pragma unroll
     for (int i = 0; i < N; ++i) Elem<T>::load(r[i], f + i * Elem<T>::E);
   }
+  // Magnitudes order like their bits, so the largest is taken on the words
+  // (16-bit types: in both halves) with a NaN above infinity.
+  __device__ __forceinline__ uint32_t top(uint32_t m) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const uint32_t w[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if constexpr (sizeof(T) == 4) m = max(m, w[q] & 0x7fffffffu);
+        else m = __vmaxu2(m, w[q] & 0x7fff7fffu);
+      }
+    }
+    return m;
+  }
+  // That maximum as a float; a NaN if there was one.
+  static __device__ __forceinline__ float value(uint32_t m) {
+    if constexpr (sizeof(T) == 4) {
+      return __uint_as_float(m);
+    } else {
+      const unsigned short u = (unsigned short)max(m & 0xffffu, m >> 16);
+      T x;
+      memcpy(&x, &u, 2);
+      return (float)x;
+    }
+  }
+  __device__ __forceinline__ bool has_nan() const {
+    return isnan(value(top(0)));
+  }
+  __device__ __forceinline__ void clear_nans() {
+    T one[8];
+    memcpy(one, r, sizeof(r));
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (isnan((float)one[i])) one[i] = (T)0.f;
+    memcpy(r, one, sizeof(r));
+  }
 };
 
 template <int D> constexpr int append_threads() { return D == 256 ? 256 : 128; }
 
 template <typename T, int D, bool VEC>
-__global__ void __launch_bounds__(append_threads<D>(), D == 256 ? 3 : 6) append_kernel(const KvAppend a) {
+__global__ void __launch_bounds__(append_threads<D>(), D == 256 ? 3 : 5) append_kernel(const KvAppend a) {
   constexpr int TH = append_threads<D>(), NW = TH / 32;
   constexpr int CH = D / 8;                // groups of 8 elements in a token
   constexpr int G = 16 * CH / TH;          // (word of 4 tokens, 8 elements) per thread
@@ -423,6 +463,7 @@ __global__ void __launch_bounds__(append_threads<D>(), D == 256 ? 3 : 6) append_
   __shared__ float red[NW];
   __shared__ int nan_s[kKvPage];
   __shared__ int item_s[2];
+  extern __shared__ __align__(16) uint4 staged[];  // VEC: the keys, each thread's own pieces at [piece][thread]
   const int tid = threadIdx.x, h = blockIdx.x % a.kv.H;
   const int unit = blockIdx.x / a.kv.H;
   if (*a.kv.err != 0) return;
@@ -515,20 +556,33 @@ __global__ void __launch_bounds__(append_threads<D>(), D == 256 ? 3 : 6) append_
       }
   };
   // side 0: values (their NaNs mark the keys), 1: keys
-  auto write = [&](int side, const Raw8<T> (&x)[G][4]) {
+  auto write = [&](int side, Raw8<T> (&x)[G][4]) {
     float* scale_p = (side == 0 ? a.kv.v_scale : a.kv.k_scale) + block;
     uint8_t* codes = (side == 0 ? a.kv.v : a.kv.k) + block * kKvPage * D;
     const float had = off > 0 ? *scale_p : 0.f;  // a page's first token starts it afresh
-    float top = 0.f;
+    uint32_t most = 0, nans = 0;
 #pragma unroll
     for (int g = 0; g < G; ++g)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float f[8];
-        x[g][i].get(f);
+      for (int i = 0; i < 4; ++i) most = x[g][i].top(most);
+    float top = Raw8<T>::value(most);
+    if (isnan(top)) {
+      // seldom: the largest of what is no NaN; values count a NaN as zero and mark its token
+      top = 0.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[e]));  // fmaxf passes over a NaN
-      }
+      for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float f[8];
+          x[g][i].get(f);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[e]));  // fmaxf passes over a NaN
+          if (side == 0 && x[g][i].has_nan()) {
+            nans |= 1u << (g * 4 + i);
+            x[g][i].clear_nans();
+          }
+        }
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     __syncthreads();  // red is free; everyone has read the old scale of this side, nan_s is clear
@@ -540,6 +594,13 @@ __global__ void __launch_bounds__(append_threads<D>(), D == 256 ? 3 : 6) append_
     const bool grown = off > 0 && now != had;
     const float inv = 1.f / now, ratio = had * inv;
     if (tid == 0) *scale_p = now;
+    if (nans) {
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (nans >> (g * 4 + i) & 1) nan_s[4 * word_of(g) + i] = 1;
+    }
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       const int w = word_of(g);
@@ -549,19 +610,9 @@ __global__ void __launch_bounds__(append_threads<D>(), D == 256 ? 3 : 6) append_
         const int t = 4 * w + i;
         float f[8];
         x[g][i].get(f);
-        if (side == 0) {
-          bool nan = false;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            nan |= isnan(f[e]);
-            f[e] = isnan(f[e]) ? 0.f : f[e] * inv;
-          }
-          if (nan) nan_s[t] = 1;
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] *= inv;
-          if (d == 0 && nan_s[t]) f[0] = __int_as_float(0x7fffffff);
-        }
+        for (int e = 0; e < 8; ++e) f[e] *= inv;
+        if (side == 1 && d == 0 && nan_s[t]) f[0] = __int_as_float(0x7fffffff);
         c[i][0] = f32x2_to_e4m3x2(f[0], f[1]) | (f32x2_to_e4m3x2(f[2], f[3]) << 16);
         c[i][1] = f32x2_to_e4m3x2(f[4], f[5]) | (f32x2_to_e4m3x2(f[6], f[7]) << 16);
         if (side == 1 && t >= off && t < end)
@@ -591,6 +642,16 @@ __global__ void __launch_bounds__(append_threads<D>(), D == 256 ? 3 : 6) append_
       __syncthreads();
       // words of 4 tokens: whole new ones are written, others merged with
       // what is there (rescaled before the first new token if the scale grew)
+      if (off == 0 && end == kKvPage) {
+#pragma unroll
+        for (int i = tid; i < D * 4; i += TH) {
+          const int e = i / 4, w = 4 * (i % 4), x = e / 8 % 16;
+          const uint32_t* row = vt + e * 16;
+          *reinterpret_cast<uint4*>(codes + e * kKvPage + 4 * w) =
+              make_uint4(row[w ^ x], row[(w + 1) ^ x], row[(w + 2) ^ x], row[(w + 3) ^ x]);
+        }
+        return;
+      }
       const int w0 = grown ? 0 : off / 4, nw = (end + 3) / 4 - w0;
       for (int i = tid; i < nw * D; i += TH) {
         const int e = i / nw, w = w0 + i % nw;
@@ -612,9 +673,38 @@ __global__ void __launch_bounds__(append_threads<D>(), D == 256 ? 3 : 6) append_
   };
   Raw8<T> x[G][4];
   load(0, x);
-  write(0, x);
-  load(1, x);
-  write(1, x);
+  if constexpr (VEC) {
+    // the keys are under way while the values are worked on
+    constexpr int N = Raw8<T>::N;
+    const T* src = static_cast<const T*>(a.k) + (long long)h * a.k_head + d;
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int t = 4 * word_of(g) + i;
+        const bool in = t >= off && t < end;
+        const uint4* from = reinterpret_cast<const uint4*>(src + (in ? (long long)(tok0 + t) * a.k_tok : 0));
+#pragma unroll
+        for (int n = 0; n < N; ++n)  // outside [off, end) nothing is read and zeros are written
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                           smem_addr(staged + ((g * 4 + i) * N + n) * TH + tid)),
+                       "l"(from + n), "r"(in ? 16 : 0)
+                       : "memory");
+      }
+    write(0, x);
+    asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int n = 0; n < N; ++n) x[g][i].r[n] = staged[((g * 4 + i) * N + n) * TH + tid];
+    write(1, x);
+  } else {
+    write(0, x);
+    load(1, x);
+    write(1, x);
+  }
 }
 
 // ---- host side -------------------------------------------------------------------------
@@ -703,10 +793,18 @@ np_status copy_pages(const np_kv_desc* d, long long most, int remap, cudaStream_
   return launched(call);
 }
 
+template <typename T, int D> struct AppendTag {};
+
 template <typename T, int D>
 cudaError_t launch_append(const KvAppend& a, unsigned grid, bool vec, cudaStream_t st) {
-  if (vec) append_kernel<T, D, true><<<grid, append_threads<D>(), 0, st>>>(a);
-  else append_kernel<T, D, false><<<grid, append_threads<D>(), 0, st>>>(a);
+  if (vec) {
+    constexpr size_t staged = (size_t)kKvPage * D * sizeof(T);
+    cudaError_t e = ensure_dyn_smem<AppendTag<T, D>>(reinterpret_cast<const void*>(append_kernel<T, D, true>), staged);
+    if (e != cudaSuccess) return e;
+    append_kernel<T, D, true><<<grid, append_threads<D>(), staged, st>>>(a);
+  } else {
+    append_kernel<T, D, false><<<grid, append_threads<D>(), 0, st>>>(a);
+  }
   return cudaGetLastError();
 }
 
