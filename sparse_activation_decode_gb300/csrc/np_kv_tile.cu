@@ -353,6 +353,24 @@ __device__ __forceinline__ void sts64(uint32_t addr, uint32_t a, uint32_t b) {
   asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
 }
 
+__device__ __forceinline__ void sts_words(uint32_t addr, const uint32_t (&w)[1]) {
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(w[0]) : "memory");
+}
+__device__ __forceinline__ void sts_words(uint32_t addr, const uint32_t (&w)[2]) { sts64(addr, w[0], w[1]); }
+__device__ __forceinline__ void sts_words(uint32_t addr, const uint32_t (&w)[4]) { sts128(addr, w[0], w[1], w[2], w[3]); }
+__device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[1]) {
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[2]) {
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[4]) {
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+               : "r"(addr)
+               : "memory");
+}
+
 // 16 bytes of T from floats.
 template <typename T> __device__ __forceinline__ uint4 pack_chunk(const float* f);
 template <> __device__ __forceinline__ uint4 pack_chunk<float>(const float* f) {
@@ -400,7 +418,6 @@ struct TileShared {
   uint64_t drained[4];
   StepMeta meta[kMetaSlots];
   long long tmp[3];
-  float fac[2][128];  // factor of each row's logits
   uint32_t tmem;
   int abort;
 };
@@ -797,9 +814,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const KvAt
         const float o_l = l, o_ref = ref, o_unit = unit;
         T* const o_out = out;
         const int o_steps = in_stretch;
-        if ((flags & 1) && !skip) {
-          // the next stretch's queries first: its first product runs while
-          // the last one's results are taken
+        const bool more = (flags & 1) && !skip;
+        // The tile's part of Q: rows of 128 bytes, in blocks of 128 rows; a
+        // row of D elements takes its bytes from as many blocks.
+        const uint32_t q_rows = q_s + X * NP * Sh::kQ + (warp & 3) * 4096;
+        if (more) {
+          // the next stretch's queries, on their way to their place while the
+          // last one's results are taken (its products with Q are done)
           const StepMeta& m = sh.meta[mcount % kMetaSlots];
           const int at = m.row0 + X * 128 + row;             // row of the sequence and head
           const int tok = at / g, head = m.h * g + at % g;
@@ -810,73 +831,32 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const KvAt
               static_cast<const T*>(a.q) + (long long)(m.begin + tok) * a.q_tok + (long long)head * a.q_head;
           out = static_cast<T*>(a.out) + (long long)(m.begin + tok) * a.o_tok + (long long)head * a.o_head;
           // The warp reads its 32 rows together, 16 bytes a lane (a thread
-          // per row took 35000 cycles for a tile), and scales each so that
-          // its largest element is in [2^14, 2^15).
+          // per row took 35000 cycles for a tile).
           constexpr int E = Elem<T>::E, LPR = D / E, RPL = 32 / LPR;  // elements per lane, lanes per row, rows per load
           const unsigned in_mask = __ballot_sync(0xffffffffu, in);
           const bool wide_ok = __all_sync(0xffffffffu, !in || (reinterpret_cast<uintptr_t>(q) & 15) == 0);
-          const int d = lane % LPR * E;
-#pragma unroll 1
-          for (int i0 = 0; i0 < LPR; i0 += 8) {
-            uint4 raw[8];
+          const int ck = lane % LPR;
+#pragma unroll 2
+          for (int i = 0; i < LPR; ++i) {
+            const int r = i * RPL + lane / LPR;
+            const T* src =
+                reinterpret_cast<const T*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(q), r)) + ck * E;
+            const bool have = (in_mask >> r) & 1;
+            const uint32_t dst = q_rows + (ck >> 3) * 16384u + r * 128u + (ck & 7) * 16u;
+            if (rare(!wide_ok)) {
+              uint4 raw = make_uint4(0, 0, 0, 0);
+              if (have) {
+                T* one = reinterpret_cast<T*>(&raw);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int r = (i0 + i) * RPL + lane / LPR;
-              const T* src = reinterpret_cast<const T*>(
-                                 __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(q), r)) + d;
-              raw[i] = make_uint4(0, 0, 0, 0);
-              if ((in_mask >> r) & 1) {
-                if (wide_ok) {
-                  raw[i] = *reinterpret_cast<const uint4*>(src);
-                } else {
-                  T* one = reinterpret_cast<T*>(&raw[i]);
-#pragma unroll
-                  for (int e = 0; e < E; ++e) one[e] = src[e];
-                }
+                for (int e = 0; e < E; ++e) one[e] = src[e];
               }
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int r = (i0 + i) * RPL + lane / LPR, trow = (warp & 3) * 32 + r;
-              float x[E], top = 0.f;
-              Elem<T>::load(raw[i], x);
-#pragma unroll
-              for (int e = 0; e < E; ++e) top = fmaxf(top, fabsf(x[e]));
-#pragma unroll
-              for (int o = LPR / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-              int ex = (int)(__float_as_uint(top) >> 23) - 127;
-              ex = ex < -112 ? -112 : ex;
-              const float up = __uint_as_float((uint32_t)(14 - ex + 127) << 23);
-              if (lane % LPR == 0)
-                sh.fac[X][trow] = __uint_as_float((uint32_t)(ex - 14 + 127) << 23) * a.scale_log2;
-              uint32_t h[E / 2], lo[E / 2];
-#pragma unroll
-              for (int e = 0; e < E / 2; ++e) {
-                const float x0 = x[2 * e] * up, x1 = x[2 * e + 1] * up;
-                h[e] = pack_f16(x0, x1);
-                const float2 f = f16x2_to_f32x2(h[e]);
-                lo[e] = pack_f16(x0 - f.x, x1 - f.y);
-              }
-              const uint32_t off = X * NP * Sh::kQ + (d >> 6) * 16384u + trow * 128u +
-                                   ((((d & 63) >> 3) ^ (trow & 7)) << 4);
-              if constexpr (NP == 1) {
-                sts128(q_s + off, h[0], h[1], h[2], h[3]);
-              } else {
-                sts64(q_s + off + (d & 4) * 2, h[0], h[1]);
-                sts64(q_s + off + Sh::kQ + (d & 4) * 2, lo[0], lo[1]);
-              }
+              sts128(dst, raw.x, raw.y, raw.z, raw.w);
+            } else {
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(have ? src : static_cast<const T*>(a.q)),
+                           "r"(have ? 16 : 0)
+                           : "memory");
             }
           }
-          __syncwarp();
-          fac = sh.fac[X][(warp & 3) * 32 + lane];
-          ref = -INFINITY;
-          l = 0.f;
-          unit = NAN;
-          w_min = __reduce_min_sync(0xffffffffu, in ? pos : INT_MAX);
-          w_max = __reduce_max_sync(0xffffffffu, pos);
-          fence_proxy_async_cta();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_local(smem_addr(&sh.qready[X]));
         }
         if (flags & 1) free_entry();
         if (done_flags) {
@@ -930,6 +910,68 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const KvAt
           }
           tc_fence_before();  // before the next stretch's products overwrite O
           done_flags = 0;
+        }
+        if (more) {
+          // Each row is scaled so that its largest element is in [2^14, 2^15),
+          // and goes from the order it came in to the operand's.
+          constexpr int QE = D / 32, QW = QE * sizeof(T) / 4;  // elements, words of a row per lane
+          asm volatile("cp.async.wait_all;" ::: "memory");
+          __syncwarp();
+          const uint32_t from = q_rows + (lane * QW >> 5) * 16384u + (lane * QW & 31) * 4u;
+          const int d = lane * QE;
+#pragma unroll 1
+          for (int r0 = 0; r0 < 32; r0 += 4) {
+            uint32_t w[4][QW], most[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) lds_words(from + (r0 + i) * 128, w[i]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              // magnitudes order like their bits (a NaN above infinity)
+              uint32_t m = 0;
+#pragma unroll
+              for (int e = 0; e < QW; ++e)
+                m = NP == 2 ? max(m, w[i][e] & 0x7fffffffu) : __vmaxu2(m, w[i][e] & 0x7fff7fffu);
+              if constexpr (NP == 1) m = max(m & 0xffffu, m >> 16);
+              most[i] = __reduce_max_sync(0xffffffffu, m);
+            }
+            __syncwarp();  // the rows are read before they are written
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int r = r0 + i;
+              float top = __uint_as_float(most[i]);
+              if constexpr (NP == 1) {
+                const unsigned short u = (unsigned short)most[i];
+                T t;
+                memcpy(&t, &u, 2);
+                top = (float)t;
+              }
+              int ex = (int)(__float_as_uint(top) >> 23) - 127;
+              ex = ex < -112 ? -112 : ex;
+              const float up = __uint_as_float((uint32_t)(14 - ex + 127) << 23);
+              if (r == lane) fac = __uint_as_float((uint32_t)(ex - 14 + 127) << 23) * a.scale_log2;
+              T x[QE];
+              memcpy(x, w[i], sizeof(x));
+              uint32_t h[QE / 2], lo[QE / 2];
+#pragma unroll
+              for (int e = 0; e < QE / 2; ++e) {
+                const float x0 = (float)x[2 * e] * up, x1 = (float)x[2 * e + 1] * up;
+                h[e] = pack_f16(x0, x1);
+                const float2 f = f16x2_to_f32x2(h[e]);
+                lo[e] = pack_f16(x0 - f.x, x1 - f.y);
+              }
+              const uint32_t to = q_rows + (d >> 6) * 16384u + r * 128u + ((((d & 63) >> 3) ^ (r & 7)) << 4) + (d & 7) * 2;
+              sts_words(to, h);
+              if constexpr (NP == 2) sts_words(to + Sh::kQ, lo);
+            }
+          }
+          ref = -INFINITY;
+          l = 0.f;
+          unit = NAN;
+          w_min = __reduce_min_sync(0xffffffffu, in ? pos : INT_MAX);
+          w_max = __reduce_max_sync(0xffffffffu, pos);
+          fence_proxy_async_cta();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_local(smem_addr(&sh.qready[X]));
         }
         if (flags & 4) break;
       }
