@@ -490,7 +490,7 @@ typedef struct {
 
 /* Attention of the new tokens of one layer: query head h reads key/value head
  * h / (n_heads / n_kv_heads); the query at position p sees keys j <= p and,
- * with window > 0, of those only j > p - window and j < sinks.
+ * with window > 0, of those only the keys with j > p - window or j < sinks.
  *   out = sum_j softmax_j(scale * q . k_j) v_j, and 0 where no key is visible.
  * Sums, maxima and the accumulator are fp32.  Keys in pages that the table
  * does not name (-1: given back under a window) are not visible. */

@@ -23,13 +23,26 @@
 // 0 and 1 (a thread per row, no exchange between threads), warps 8-11 widen
 // the pages from global memory into the swizzled operands, warps 12
 // and 14 issue the products S of tile 0 and 1 and warp 15 the products P V,
-// warp 13 walks the work list and looks up pages and scales.  S is
+// warp 13 walks the work list and looks up pages and scales.  The queries of
+// the next stretch are copied into their place while the last one's results
+// go out, and scaled there by a short loop: straight-line code that runs once
+// a stretch costs more than it computes (with the rows in registers, 265 us
+// for the first case below).  S is
 // held twice per tile: the products of the next page run while the weights of
 // this one are formed, so neither waits for the other's latency.  (With one S
 // of 128 keys per tile instead, a step's S -> weights -> P V -> S chain was
 // 6300 cycles for 4 x 512 cycles of products.)
 // Bound: the tensor cores, 4 D flops per visible (query head, key); next
 // shared memory (operands of S from both tiles, the widened pages' writes).
+// What holds it is the length of a step: about 2400 cycles for two tiles
+// whose products take 1024 (a row's weights 1100, the load of S 330, the wait
+// for it 330), and 14 k cycles where a stretch of steps ends and the next one
+// begins (queries 7 k, results 5 to 7 k).
+// Measured: 2048 tokens after 6144, 32 heads of 128, bf16: 243 us, 990
+// TFLOP/s; 2 x 4096 after 4096, 32 query heads on 8, fp16, window of 1024 and
+// 4 first keys: 215 us, 581 TFLOP/s; 3 x 173 tokens after about 900, 12 heads
+// of 64 on 4, fp16: 28.7 us.
+//
 //
 // Work split: the steps of all (sequence, head, row tile) items form one
 // list, cut into equal shares as in the streaming kernel; what a tile cannot
