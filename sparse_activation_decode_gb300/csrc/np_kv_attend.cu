@@ -35,8 +35,8 @@
 // are not cut (see plan()).
 //
 // Bound: HBM, 2 D bytes per visible token and head; for few pages the chain
-// lengths -> table -> scales and page -> products -> join (6.6 us for one
-// sequence of 200 tokens, 6 of them before the last page is read).
+// lengths -> table -> scales and page -> products -> result (6.6 us for one
+// sequence of 200 tokens).
 // Measured, single tokens: 8 sequences of up to 32768, 40 heads of 128, bf16:
 // 311 us, 6.85 TB/s; 8 of up to 4096, 32 heads: 44 us, 4.9 TB/s; one of 131071,
 // 32 query heads on 8, fp16: 56 us, 4.75 TB/s; 8 under a window of 4096, 32
