@@ -155,6 +155,27 @@ def test_a_search_with_forks_copies_release_and_compaction():
         p.attend_close([3, 1], 4, "f32", seqs=[5, 2], window=20, sinks=1)
 
 
+@pytest.mark.parametrize("width", [341, 342], ids=["one-launch", "two-launches"])
+def test_forks_of_few_and_many_entries(width):
+    from sparse_activation_decode_gb300 import NpError
+    p = Pair(P=40, H=1, D=64, B=6, W=width)
+    p.grow([200, 1, 64, 0, 130, 63])
+    p.fork([0, 0, 4, 2, 4, 1], [0, 1, 2, 3, 4, 5])
+    p.same()
+    p.fork([5, 4], [0, 3])
+    p.same()
+    p.grow([1] * 6)
+    p.same()
+    p.attend_close([1] * 6, 2, "bf16")
+    before = p.c.table.clone(), p.c.lengths.clone(), p.c.refs.clone()
+    for src, dst in (([0, 1], [2, 2]), ([0, 6], [1, 2]), ([0, 1], [-1, 2])):
+        p.c.fork(i32(src), i32(dst))
+        with pytest.raises(NpError) as e:
+            p.c.check()
+        assert e.value.status == -6
+    assert all(torch.equal(a, b) for a, b in zip(before, (p.c.table, p.c.lengths, p.c.refs)))
+
+
 def test_reserve_takes_all_or_nothing():
     from sparse_activation_decode_gb300 import NpError
     p = Pair(P=4, B=3, W=3)
