@@ -27,6 +27,7 @@ _DTYPES = {torch.float32: L.NP_F32, torch.float16: L.NP_F16, torch.bfloat16: L.N
 _current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
 _current_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+_capturing = torch.cuda.is_current_stream_capturing
 
 
 class KvCache:
@@ -104,6 +105,7 @@ class KvCache:
         self._index = self.device.index
         self._scale = 1.0 / math.sqrt(dim)
         self._ws_bytes = {}  # workspace sizes by (heads, most new tokens, dtype)
+        self._ws = {}        # workspaces by stream: (pointer, bytes, tensor)
 
     # -- argument checks (short: a decode step makes these calls per layer) -----
     def _stream(self) -> int:
@@ -202,11 +204,13 @@ class KvCache:
         n, heads, q0, q1, code = self._tokens(q, None, "q")
         if out is None:
             out = torch.empty_like(q)
-        elif n and _spans_overlap(q, out):
-            raise ValueError("out may not share memory with q")
-        if out.dtype != q.dtype or out.shape != q.shape:
-            raise ValueError("out must have q's shape and dtype")
-        _, _, o0, o1, _ = self._tokens(out, heads, "out")
+            o0, o1, _ = out.stride()
+        else:
+            if n and _spans_overlap(q, out):
+                raise ValueError("out may not share memory with q")
+            if out.dtype != q.dtype or out.shape != q.shape:
+                raise ValueError("out must have q's shape and dtype")
+            _, _, o0, o1, _ = self._tokens(out, heads, "out")
         b = self._batch(n, cu, seqs, max_q)
         key = (heads, b.max_tokens, code)
         n_ws = self._ws_bytes.get(key)
@@ -215,8 +219,15 @@ class KvCache:
             if n_ws < 0:
                 raise ValueError(f"{heads} query heads over {self.n_kv_heads} key heads are not supported")
             self._ws_bytes[key] = n_ws
-        ws = torch.empty(n_ws, dtype=torch.uint8, device=self.device)
-        t = L.KvAttn(q.data_ptr(), out.data_ptr(), q0, q1, o0, o1, ws.data_ptr(), n_ws, heads, code,
+        # Calls on one stream run one after another and share a workspace; a
+        # captured call, whose graph may be replayed on any stream, has its own.
+        ws = self._ws.get(st)
+        if ws is None or ws[1] < n_ws or _capturing():
+            t = torch.empty(n_ws, dtype=torch.uint8, device=self.device)
+            ws = (t.data_ptr(), n_ws, t)
+            if not _capturing():
+                self._ws[st] = ws
+        t = L.KvAttn(q.data_ptr(), out.data_ptr(), q0, q1, o0, o1, ws[0], ws[1], heads, code,
                      self._scale if scale is None else scale, window, sinks)
         L.check(self.lib.np_kv_attend(self._desc, layer, ctypes.byref(b), ctypes.byref(t), st), "np_kv_attend")
         return out

@@ -675,3 +675,31 @@ def test_offsets_beyond_32_bits():
     small.reserve(i32([0, 1, 0]))
     assert torch.equal(a, small.attend(0, q, cu=cu_of(m)))
     small.check()
+
+
+def test_workspaces_of_eager_and_captured_calls():
+    """Eager calls of one stream share a workspace, other streams and captured calls have their own."""
+    p = Pair(P=60, H=2, D=64, B=2, W=25)
+    p.grow([1500, 900])
+    q = {n: torch.randn(2 * n, 8, 64, device="cuda", dtype=torch.float16) for n in (1, 80)}
+    want = {n: p.c.attend(0, x) for n, x in q.items()}          # 80 rows a head: another kernel, a larger workspace
+    at = {ws[0] for ws in p.c._ws.values()}
+    assert len(at) == 1
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        p.c.attend(0, q[1])
+    assert len({ws[0] for ws in p.c._ws.values()}) == 2
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        got = {n: p.c.attend(0, x) for n, x in q.items()}
+    assert len(p.c._ws) == 2
+    torch.cuda.synchronize()
+    for _ in range(10):                                         # a replay beside eager calls on two streams
+        with torch.cuda.stream(side):
+            g.replay()
+        mine = {n: p.c.attend(0, x) for n, x in q.items()}
+        torch.cuda.synchronize()
+        for n in q:
+            assert torch.equal(want[n], got[n]) and torch.equal(want[n], mine[n])
+    p.c.check()
