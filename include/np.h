@@ -473,7 +473,7 @@ np_status np_kv_append(const np_kv_desc* kv, int32_t layer, const np_kv_batch* b
 /* What np_kv_attend reads and writes. */
 typedef struct {
   const void* q;             /* [n_tokens][n_heads][head_dim] of dtype */
-  void* out;                 /* the same; shares no memory with q */
+  void* out;                 /* the same; shares no memory with q, and no two of its rows any */
   int64_t q_token_stride;    /* strides in elements; the last dimension is contiguous */
   int64_t q_head_stride;
   int64_t out_token_stride;
@@ -483,7 +483,7 @@ typedef struct {
   int32_t n_heads;           /* query heads: a multiple of n_kv_heads, at most 1024; n_tokens *
                                 n_heads / n_kv_heads below 2^30 */
   int32_t dtype;             /* NP_F32, NP_F16 or NP_BF16 */
-  float scale;               /* > 0 */
+  float scale;               /* > 0; scale * log2(e) finite */
   int32_t window;            /* 0: every key up to the query's position */
   int32_t sinks;             /* first keys that stay visible under a window */
 } np_kv_attn;

@@ -962,7 +962,8 @@ extern "C" np_status np_kv_attend(const np_kv_desc* d, int32_t layer, const np_k
     return kv_fail(NP_ERR_ARG, "np_kv_attend: bad layer or dtype");
   if (t->n_heads < 1 || t->n_heads > 1024 || t->n_heads % d->n_kv_heads)
     return kv_fail(NP_ERR_ARG, "np_kv_attend: n_heads is not a multiple of the cache's heads");
-  if (!std::isfinite(t->scale) || t->scale <= 0.f || t->window < 0 || t->sinks < 0)
+  const float scale_log2 = t->scale * 1.4426950408889634f;
+  if (!std::isfinite(scale_log2) || t->scale <= 0.f || t->window < 0 || t->sinks < 0)
     return kv_fail(NP_ERR_ARG, "np_kv_attend: bad scale, window or sinks");
   if ((int64_t)b->n_tokens * (t->n_heads / d->n_kv_heads) >= (1ll << 30))
     return kv_fail(NP_ERR_ARG, "np_kv_attend: too many tokens for one call");
@@ -971,12 +972,14 @@ extern "C" np_status np_kv_attend(const np_kv_desc* d, int32_t layer, const np_k
   if (!t->q || !t->out || !aligned(t->q, esz) || !aligned(t->out, esz) || t->q_token_stride < 0 ||
       t->q_head_stride < 0 || t->out_token_stride < 0 || t->out_head_stride < 0)
     return kv_fail(NP_ERR_ARG, "np_kv_attend: bad tensors");
+  if ((b->n_tokens > 1 && t->out_token_stride < d->head_dim) || (t->n_heads > 1 && t->out_head_stride < d->head_dim))
+    return kv_fail(NP_ERR_ARG, "np_kv_attend: rows of out lie on one another");
   if (!t->workspace || !aligned(t->workspace, 16) ||
       t->workspace_bytes <
           (int64_t)kv_attend_workspace(t->dtype, d->head_dim, (long long)b->max_tokens * (t->n_heads / d->n_kv_heads)))
     return kv_fail(NP_ERR_ARG, "np_kv_attend: workspace missing, unaligned or too small");
   KvAttend a{view_of(d, layer), batch_of(b), t->q, t->out, t->q_token_stride, t->q_head_stride,
-             t->out_token_stride, t->out_head_stride, t->n_heads, t->dtype, t->scale * 1.4426950408889634f,
+             t->out_token_stride, t->out_head_stride, t->n_heads, t->dtype, scale_log2,
              t->window, t->sinks, t->workspace};
   const cudaError_t e = launch_kv_attend(a, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? NP_OK : kv_fail(NP_ERR_CUDA, cudaGetErrorString(e));

@@ -92,6 +92,13 @@ def test_bad_attention_arguments_are_refused(lib, kw):
                             None) == L.NP_ERR_ARG
 
 
+@pytest.mark.parametrize("kw", [dict(out_token_stride=0), dict(out_token_stride=127), dict(out_head_stride=0),
+                                dict(out_head_stride=127), dict(scale=3e38)], ids=str)
+def test_rows_of_out_on_one_another_and_scales_too_large_are_refused(lib, kw):
+    assert lib.np_kv_attend(ctypes.byref(desc()), 0, ctypes.byref(batch()), ctypes.byref(attn(lib, **kw)),
+                            None) == L.NP_ERR_ARG
+
+
 def test_bad_layers_lists_and_tensors_are_refused(lib):
     d, b, t = ctypes.byref(desc()), ctypes.byref(batch()), ctypes.byref(attn(lib))
     for layer in (-1, 2):
