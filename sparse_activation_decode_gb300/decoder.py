@@ -148,7 +148,8 @@ class SparseDecoder:
         issued layer by layer (predictor after layer 0, each sparse layer's
         reads on the side stream while earlier layers run) instead of as the
         captured token; the per-layer predictor sees the layer's input after
-        `mix`.  `stats` and a lookahead are not available with it."""
+        `mix`.  If it raises, h is left part of the way and the decoder can
+        take the next step.  `stats` and a lookahead are not available with it."""
         if mix is not None:
             return self._decode_mixed(h, stats, mix)
         self._on_main(h)
@@ -168,19 +169,26 @@ class SparseDecoder:
             raise ValueError("h must be a contiguous float32 CUDA tensor of batch * d_model elements")
         shared = self.pred_kind == "shared_argmax"
         self._on_main(h)
-        with torch.cuda.stream(self.main_stream):
-            for layer in range(self.n_layers):
-                sparse = layer >= self.n_dense
-                if sparse and shared:
-                    self.scatter(layer)
-                mix(layer, h)
-                if sparse and not shared:
-                    self.delta(self.predict(h, layer), layer)
-                    self.scatter(layer)
-                self.ffn_layers(layer, 1, h)
-                if layer == 0 and shared and self.n_sparse:
-                    self.delta(self.predict(h), -1)
-        self._back()
+        try:
+            with torch.cuda.stream(self.main_stream):
+                for layer in range(self.n_layers):
+                    sparse = layer >= self.n_dense
+                    if sparse and shared:
+                        self.scatter(layer)
+                    mix(layer, h)
+                    if sparse and not shared:
+                        self.delta(self.predict(h, layer), layer)
+                        self.scatter(layer)
+                    self.ffn_layers(layer, 1, h)
+                    if layer == 0 and shared and self.n_sparse:
+                        self.delta(self.predict(h), -1)
+        except BaseException:
+            # the rows of layers that the step did not come to are read all
+            # the same, so that the next step finds what the slot maps say
+            self.lib.np_scatter(self.model, -1)
+            raise
+        finally:
+            self._back()
 
     def predict(self, h: torch.Tensor, layer: int = 0) -> torch.Tensor:
         self._on_main(h)

@@ -101,3 +101,24 @@ def test_mix_refusals():
     with pytest.raises(ValueError):
         dec.decode_token(opt.x[0].cuda().clone(), mix=lambda layer, y: None)
     dec.close()
+
+
+@pytest.mark.parametrize("cfg", [SMALL_F16, SMALL_OPT, SMALL_F16.replace(slots="compact")],
+                         ids=lambda c: f"{c.name}-{c.slots}")
+def test_a_mix_that_raises_leaves_a_decoder_that_goes_on(cfg):
+    wl = make_workload(cfg)
+    a, b = build_decoder(wl), build_decoder(wl)
+    for t in range(3):
+        for stop in (0, 1, cfg.n_layers - 1):
+            def mix(layer, h):
+                if layer == stop:
+                    raise KeyError(layer)
+            with pytest.raises(KeyError):
+                b.decode_token(wl.x[t].cuda().clone(), mix=mix)
+        x, y = wl.x[t].cuda().clone(), wl.x[t].cuda().clone()
+        a.decode_token(x)
+        b.decode_token(y, mix=(lambda layer, h: None) if t == 1 else None)
+        torch.cuda.synchronize()
+        assert oracle.rel_l2(y.cpu().numpy().ravel(), x.cpu().numpy().ravel()) <= 1e-5
+    a.close()
+    b.close()
