@@ -40,8 +40,8 @@
 // begins (queries 7 k, results 5 to 7 k).
 // Measured: 2048 tokens after 6144, 32 heads of 128, bf16: 243 us, 990
 // TFLOP/s; 2 x 4096 after 4096, 32 query heads on 8, fp16, window of 1024 and
-// 4 first keys: 215 us, 581 TFLOP/s; 3 x 173 tokens after about 900, 12 heads
-// of 64 on 4, fp16: 28.7 us.
+// 4 first keys: 212 us, 590 TFLOP/s; 3 x 173 tokens after about 900, 12 heads
+// of 64 on 4, fp16: 25.1 us.
 //
 //
 // Work split: the steps of all (sequence, head, row tile) items form one
@@ -93,7 +93,7 @@ struct TileSeq {
 
 struct TilePlan {
   long long chunk, total;
-  int split;
+  int split, rows;  // rows: of a tile item
 };
 
 // Keys that a tile's rows see, as a list of pages: slots [0, sink), [lo, ..).
@@ -102,8 +102,7 @@ struct TileKeys {
   __device__ __forceinline__ int slot(int k) const { return k < sink ? k : lo + (k - sink); }
 };
 
-template <int R>
-__device__ __forceinline__ TileKeys tile_keys(const KvAttend& a, int n, int len, int tile) {
+__device__ __forceinline__ TileKeys tile_keys(const KvAttend& a, int R, int n, int len, int tile) {
   const int g = a.Hq / a.kv.H;
   const long long all = n * (long long)g, first = (long long)tile * R;
   TileKeys t;
@@ -131,7 +130,10 @@ __device__ __forceinline__ int tiles_of(const KvAttend& a, int n, int R) {
 
 // Numbers the units (steps, or whole items where nothing is to be gained by
 // cutting): pre[i] = units before sequence i, every head of a sequence having
-// as many.  Called by the whole CTA.
+// as many.  Where all items of 128 rows have a CTA of their own, an item is
+// one tile of 128 and not two: a step of one tile takes 1800 cycles, of two
+// 2400 (3 x 173 tokens, 12 heads of 64 on 4: 25.1 us, 28.7 with two).  Called by the
+// whole CTA.
 template <int R>
 __device__ __forceinline__ TilePlan tile_plan(const KvAttend& a, int ctas, long long* pre, TileSeq* seq,
                                               long long* tmp) {
@@ -148,7 +150,7 @@ __device__ __forceinline__ TilePlan tile_plan(const KvAttend& a, int ctas, long 
     long long steps = 0;
     int longest = 0;
     for (int t = lane; t < tiles; t += 32) {
-      const int s = tile_keys<R>(a, seq[i].n, seq[i].len, t).pages;
+      const int s = tile_keys(a, R, seq[i].n, seq[i].len, t).pages;
       steps += s;
       longest = s > longest ? s : longest;
     }
@@ -165,23 +167,26 @@ __device__ __forceinline__ TilePlan tile_plan(const KvAttend& a, int ctas, long 
   }
   __syncthreads();
   if (warp == 0) {
-    long long items = 0, steps = 0;
+    long long items = 0, steps = 0, low = 0;
     for (int i = lane; i < n; i += 32) {
       items += (long long)tiles_of(a, seq[i].n, R) * a.kv.H;
+      low += (long long)tiles_of(a, seq[i].n, 128) * a.kv.H;
       steps += pre[i] * a.kv.H;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       items += __shfl_xor_sync(0xffffffffu, items, o);
       steps += __shfl_xor_sync(0xffffffffu, steps, o);
+      low += __shfl_xor_sync(0xffffffffu, low, o);
     }
     const bool split = kv_div(items + ctas - 1, ctas) * tmp[2] > kv_div(steps, ctas) + kCutCost;
+    const int rows = !split && low <= ctas ? 128 : R;
     long long run = 0;
     for (int base = 0; base < n; base += 32) {
       const int i = base + lane;
       long long u = 0;
       if (i < n) {
-        u = (split ? pre[i] : (long long)tiles_of(a, seq[i].n, R)) * a.kv.H;
+        u = (split ? pre[i] : (long long)tiles_of(a, seq[i].n, rows)) * a.kv.H;
       }
       long long x = u;
 #pragma unroll
@@ -196,6 +201,7 @@ __device__ __forceinline__ TilePlan tile_plan(const KvAttend& a, int ctas, long 
       pre[n] = run;
       tmp[0] = kv_div(run + ctas - 1, ctas);
       tmp[1] = split;
+      tmp[2] = rows;
     }
   }
   __syncthreads();
@@ -203,6 +209,7 @@ __device__ __forceinline__ TilePlan tile_plan(const KvAttend& a, int ctas, long 
   p.chunk = tmp[0] > 0 ? tmp[0] : 1;
   p.total = pre[n];
   p.split = (int)tmp[1];
+  p.rows = (int)tmp[2];
   return p;
 }
 
@@ -214,10 +221,9 @@ struct TilePos {
 };
 
 // Unit u (called by a whole warp).
-template <int R>
 __device__ __forceinline__ TilePos tile_find(const KvAttend& a, const TilePlan& p, const long long* pre,
                                              const TileSeq* seq, long long u) {
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, R = p.rows;
   int lo = 0, hi = a.batch.n_seqs;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -234,7 +240,7 @@ __device__ __forceinline__ TilePos tile_find(const KvAttend& a, const TilePlan& 
   if (!p.split) return t;
   for (int base = 0; base < t.tiles; base += 32) {
     const int i = base + lane;
-    const int s = i < t.tiles ? tile_keys<R>(a, seq[lo].n, seq[lo].len, i).pages : 0;
+    const int s = i < t.tiles ? tile_keys(a, R, seq[lo].n, seq[lo].len, i).pages : 0;
     int x = s;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -512,18 +518,18 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const KvAt
     };
     KvCut cut{};
     if (u0 < u1) {
-      TilePos t = tile_find<R>(a, p, pre, seq, u0);
+      TilePos t = tile_find(a, p, pre, seq, u0);
       if (t.step > 0 && t.step <= p.chunk) {  // the first cut inside this item
-        const TileKeys tk = tile_keys<R>(a, seq[t.b].n, seq[t.b].len, t.tile);
+        const TileKeys tk = tile_keys(a, p.rows, seq[t.b].n, seq[t.b].len, t.tile);
         cut.more = (int)kv_div(tk.pages - t.step + p.chunk - 1, p.chunk);
-        cut.row0 = t.tile * R;
+        cut.row0 = t.tile * p.rows;
         cut.rows = tk.rows;
         cut.begin = seq[t.b].begin;
         cut.h = t.h;
       }
       for (long long u = u0; u < u1 && alive;) {
         const TileSeq w = seq[t.b];
-        const TileKeys tk = tile_keys<R>(a, w.n, w.len, t.tile);
+        const TileKeys tk = tile_keys(a, p.rows, w.n, w.len, t.tile);
         const int steps = tk.pages;
         const int s0 = t.step;
         int s1 = steps;
@@ -564,7 +570,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const KvAt
               const int s = sb + i;
               m->flags = (s == s0 ? 1 : 0) | (s == s1 - 1 ? 2 : 0) | (s0 == 0 ? 8 : 0) | (s1 == steps ? 16 : 0) |
                          ((tk.rows + 127) / 128) << 8;
-              m->row0 = t.tile * R;
+              m->row0 = t.tile * p.rows;
               m->rows = tk.rows;
               m->begin = w.begin;
               m->n = w.n;
@@ -585,7 +591,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const KvAt
             t.h = 0;
             do {
               ++t.b;
-              t.tiles = t.b < a.batch.n_seqs ? tiles_of(a, seq[t.b].n, R) : 1;
+              t.tiles = t.b < a.batch.n_seqs ? tiles_of(a, seq[t.b].n, p.rows) : 1;
             } while (t.tiles == 0);
           }
         }
