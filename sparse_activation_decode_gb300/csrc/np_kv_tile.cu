@@ -69,7 +69,12 @@ constexpr int kFold = 8;  // steps between additions into the second accumulator
 // page's value scale from O's unit, the factor on all weights.  Together they
 // stay below fp16's largest, 2^16.
 constexpr float kLazy = 6.f, kUnit = 3.f, kLift = 6.f;
-constexpr int kCutCost = 16;   // steps that cutting an item costs (partials, second launch)
+// Steps that cutting items costs: the partials of a CTA (R x D fp32 written
+// and read again) and the second launch.  Cut / whole, us: 128 tokens of 2048,
+// 32 heads of 128 on 8, 32 steps an item: 43.6 / 38.4; 2 x 64 of 3000, 47
+// steps: 45.4 / 50.7; 512 of 2048, 16 heads of 64 on 8: 33.7 / 37.2; 200 of
+// 1400, 8 heads of 256 on 2: 66 / 45; fp32, heads of 64 on 2, 13 steps: 26.9 / 22.7.
+constexpr int cut_cost(int R, int D) { return R * D / 1024 > 16 ? R * D / 1024 : 16; }
 
 // NX tiles of 128 rows, NP fp16 parts of Q and P, NB operand buffers.
 template <typename T, int D> struct TileShape {
@@ -135,7 +140,7 @@ __device__ __forceinline__ int tiles_of(const KvAttend& a, int n, int R) {
 // 2400 (3 x 173 tokens, 12 heads of 64 on 4: 25.1 us, 28.7 with two).  Called by the
 // whole CTA.
 template <int R>
-__device__ __forceinline__ TilePlan tile_plan(const KvAttend& a, int ctas, long long* pre, TileSeq* seq,
+__device__ __forceinline__ TilePlan tile_plan(const KvAttend& a, int ctas, int cut, long long* pre, TileSeq* seq,
                                               long long* tmp) {
   const int n = a.batch.n_seqs;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
@@ -179,7 +184,7 @@ __device__ __forceinline__ TilePlan tile_plan(const KvAttend& a, int ctas, long 
       steps += __shfl_xor_sync(0xffffffffu, steps, o);
       low += __shfl_xor_sync(0xffffffffu, low, o);
     }
-    const bool split = kv_div(items + ctas - 1, ctas) * tmp[2] > kv_div(steps, ctas) + kCutCost;
+    const bool split = kv_div(items + ctas - 1, ctas) * tmp[2] > kv_div(steps, ctas) + cut;
     const int rows = !split && low <= ctas ? 128 : R;
     long long run = 0;
     for (int base = 0; base < n; base += 32) {
@@ -491,8 +496,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const KvAt
     tmem_relinquish();
     tc_fence_before();
   }
+  constexpr int kCut = cut_cost(R, D);
   grid_dependency_wait();  // (launched while the kernel before may still run)
-  const TilePlan p = tile_plan<R>(a, gridDim.x, pre, seq, sh.tmp);  // synchronises the CTA
+  const TilePlan p = tile_plan<R>(a, gridDim.x, kCut, pre, seq, sh.tmp);  // synchronises the CTA
   tc_fence_after();
   grid_dependents_launch();
   const uint32_t tmem = sh.tmem;
