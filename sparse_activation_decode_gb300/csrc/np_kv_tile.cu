@@ -1151,30 +1151,57 @@ __global__ void __launch_bounds__(256) tile_join_kernel(const KvAttend a) {
   grid_dependency_wait();
   const KvCut cut = static_cast<const KvCut*>(a.ws)[blockIdx.x];
   if (cut.more == 0) return;
+  // A warp joins four rows side by side (one after the other, each partial
+  // behind the one before, took most of what cutting costs).
   const int lane = threadIdx.x & 31, c0 = blockIdx.x - 1, g = a.Hq / a.kv.H;
-  for (int i = 0; i < 4; ++i) {
-    const int row = blockIdx.y * 32 + i * 8 + (threadIdx.x >> 5);
-    if (row >= cut.rows) continue;
-    float top = TilePartial<D, R>::m(a.ws, 2 * c0 + 1)[row];
-    for (int k = 1; k <= cut.more; ++k) top = fmaxf(top, TilePartial<D, R>::m(a.ws, 2 * (c0 + k))[row]);
-    const float zero = top == -INFINITY ? 0.f : top;
-    float sum = 0.f, y[V];
+  const int row0 = blockIdx.y * 32 + (threadIdx.x >> 5) * 4;
+  if (row0 >= cut.rows) return;
+  const int n_rows = cut.rows - row0 < 4 ? cut.rows - row0 : 4;
+  auto slot_of = [&](int k) { return 2 * (c0 + k) + (k == 0 ? 1 : 0); };
+  // statistics: lane 8 i + k looks at partial k (+ 8 t) of row i
+  const int i8 = lane >> 3, k8 = lane & 7, row8 = row0 + (i8 < n_rows ? i8 : 0);
+  float top = -INFINITY;
+  for (int k = k8; k <= cut.more; k += 8) top = fmaxf(top, TilePartial<D, R>::m(a.ws, slot_of(k))[row8]);
 #pragma unroll
-    for (int j = 0; j < V; ++j) y[j] = 0.f;
-    for (int k = 0; k <= cut.more; ++k) {
-      const int slot = 2 * (c0 + k) + (k == 0 ? 1 : 0);
-      const float f = ex2(TilePartial<D, R>::m(a.ws, slot)[row] - zero);
-      sum = fmaf(TilePartial<D, R>::l(a.ws, slot)[row], f, sum);
-      const float* o = TilePartial<D, R>::o(a.ws, slot) + (size_t)row * D + lane;
+  for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const float zero = top == -INFINITY ? 0.f : top;
+  float sum = 0.f, y[4][V];
 #pragma unroll
-      for (int j = 0; j < V; ++j) y[j] = fmaf(o[32 * j], f, y[j]);
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < V; ++j) y[i][j] = 0.f;
+  for (int base = 0; base <= cut.more; base += 8) {
+    float f = 0.f;
+    if (base + k8 <= cut.more) {
+      const int slot = slot_of(base + k8);
+      f = ex2(TilePartial<D, R>::m(a.ws, slot)[row8] - zero);
+      sum = fmaf(TilePartial<D, R>::l(a.ws, slot)[row8], f, sum);
     }
-    const int at = cut.row0 + row;
+    const int here = cut.more - base < 7 ? cut.more - base + 1 : 8;
+#pragma unroll 2
+    for (int k = 0; k < here; ++k) {
+      const float* o = TilePartial<D, R>::o(a.ws, slot_of(base + k)) + (size_t)row0 * D + lane;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float fi = __shfl_sync(0xffffffffu, f, 8 * i + k);
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+          if (i < n_rows) y[i][j] = fmaf(o[i * D + 32 * j], fi, y[i][j]);
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float all = __shfl_sync(0xffffffffu, sum, 8 * i);
+    if (i >= n_rows) break;
+    const int at = cut.row0 + row0 + i;
     T* out = static_cast<T*>(a.out) + (long long)(cut.begin + at / g) * a.o_tok +
              (long long)(cut.h * g + at % g) * a.o_head;
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const float inv = all == 0.f ? 0.f : 1.f / all;
 #pragma unroll
-    for (int j = 0; j < V; ++j) out[lane + 32 * j] = kv_from_float<T>(y[j] * inv);
+    for (int j = 0; j < V; ++j) out[lane + 32 * j] = kv_from_float<T>(y[i][j] * inv);
   }
 }
 
