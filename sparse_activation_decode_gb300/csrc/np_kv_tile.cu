@@ -38,10 +38,10 @@
 // whose products take 1024 (a row's weights 1100, the load of S 330, the wait
 // for it 330), and 14 k cycles where a stretch of steps ends and the next one
 // begins (queries 7 k, results 5 to 7 k).
-// Measured: 2048 tokens after 6144, 32 heads of 128, bf16: 243 us, 990
+// Measured: 2048 tokens after 6144, 32 heads of 128, bf16: 241 us, 998
 // TFLOP/s; 2 x 4096 after 4096, 32 query heads on 8, fp16, window of 1024 and
 // 4 first keys: 212 us, 590 TFLOP/s; 3 x 173 tokens after about 900, 12 heads
-// of 64 on 4, fp16: 25.1 us.
+// of 64 on 4, fp16: 24.5 us.
 //
 //
 // Work split: the steps of all (sequence, head, row tile) items form one
@@ -71,9 +71,9 @@ constexpr int kFold = 8;  // steps between additions into the second accumulator
 constexpr float kLazy = 6.f, kUnit = 3.f, kLift = 6.f;
 // Steps that cutting items costs: the partials of a CTA (R x D fp32 written
 // and read again) and the second launch.  Cut / whole, us: 128 tokens of 2048,
-// 32 heads of 128 on 8, 32 steps an item: 43.6 / 38.4; 2 x 64 of 3000, 47
-// steps: 45.4 / 50.7; 512 of 2048, 16 heads of 64 on 8: 33.7 / 37.2; 200 of
-// 1400, 8 heads of 256 on 2: 66 / 45; fp32, heads of 64 on 2, 13 steps: 26.9 / 22.7.
+// 32 heads of 128 on 8, 32 steps an item: 41.5 / 39.2; 2 x 64 of 3000, 47
+// steps: 44.5 / 50.7; 512 of 2048, 16 heads of 64 on 8, 32 steps: 29.3 / 37.2;
+// 600 of 1100, 16 heads of 64 on 4, 18 steps: 26.2 / 24.5.
 constexpr int cut_cost(int R, int D) { return R * D / 1024 > 16 ? R * D / 1024 : 16; }
 
 // NX tiles of 128 rows, NP fp16 parts of Q and P, NB operand buffers.
